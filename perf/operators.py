@@ -211,7 +211,9 @@ def _run_own(op, case, st):
         if op == "route":
             return idx, w
         return idx, w, cco.route_grad(st["logits"], idx, st["dw"], **kw)
-    kw = dict(post=st["post"], gate=st["gate"], pre=st["pre"], scale=_SCALE, eps=_EPS)
+    kw = dict(post=st["post"], pre=st["pre"], scale=_SCALE, eps=_EPS)
+    if case["gate"] != "none":
+        kw["gate" if case["gate"] == "channel" else "token_gate"] = st["gate"]
     if op == "norm":
         out, u = cco.block_norm(st["x"], st["y"], **kw)
         return [t for t in (out, u) if t is not None]
