@@ -3,7 +3,8 @@ MI355X (gfx950).
 
 The path runs in hand-written HIP kernels behind a C ABI (include/cco_moe.h,
 built into libcco_moe.so next to this file); this package is the Python
-binding.  Importing it without the built library raises ImportError.
+binding.  The operators around the path (include/cco_ops.h) are functions:
+route, group_product and block_norm with their gradients, and combine_norm.  Importing it without the built library raises ImportError.
 """
 from ._capi import (  # noqa: F401
     CCO_ERR_BAD_EXPERT,
@@ -24,3 +25,13 @@ from ._capi import (  # noqa: F401
     status_string,
 )
 from .moe import MoE, SymHeap, device_to_host, host_to_device, required_slot_bytes  # noqa: F401
+from .ops import (  # noqa: F401
+    block_norm,
+    block_norm_grad,
+    combine_norm,
+    group_product,
+    group_product_dw,
+    group_product_dx,
+    route,
+    route_grad,
+)

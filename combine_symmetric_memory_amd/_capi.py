@@ -1,4 +1,4 @@
-"""ctypes declarations of include/cco_moe.h.
+"""ctypes declarations of include/cco_moe.h and include/cco_ops.h.
 
 Loads libcco_moe.so from this package directory.  There is no fallback:
 if the library is missing, importing raises, naming the build command.
@@ -25,6 +25,9 @@ CCO_ERR_DISABLED = -9
 CCO_NUM_KERNEL_KINDS = 10
 KERNEL_KINDS = ("plan_count", "plan_rank", "dispatch", "expert_gate_up", "expert_down",
                 "combine", "combine_copy_in", "dispatch_fp8", "stage_in_sdma", "fused")
+CCO_BF16, CCO_F16, CCO_F32 = 0, 1, 2
+CCO_SCORE_SOFTMAX, CCO_SCORE_SIGMOID = 0, 1
+CCO_GATE_NONE, CCO_GATE_CHANNEL, CCO_GATE_TOKEN = 0, 1, 2
 
 
 class cco_moe_shape(ctypes.Structure):
@@ -47,8 +50,26 @@ class cco_moe_layout(ctypes.Structure):
                 ("cap", ctypes.c_int64)]
 
 
+class cco_route_desc(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("groups", ctypes.c_int32), ("kept", ctypes.c_int32)]
+
+
+class cco_groups(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int32), ("rows", ctypes.c_int32), ("first", ctypes.c_void_p),
+                ("count", ctypes.c_void_p)]
+
+
+class cco_block_norm_desc(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("pre", ctypes.c_void_p)]
+
+
 # (name, restype, argtypes) for every symbol the header declares
 P, I32, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint64
+I64 = ctypes.c_int64
 PP = ctypes.POINTER(ctypes.c_void_p)
 SIGNATURES = [
     ("cco_sym_heap_create", ctypes.c_int, [ctypes.c_int, I32, U64, PP]),
@@ -76,6 +97,15 @@ SIGNATURES = [
     ("cco_moe_timing_summary", ctypes.c_int, [P, P, P]),
     ("cco_moe_plan_noalloc", ctypes.c_int, [P, I32, I32, I32, I32, ctypes.c_int64, P, P, P,
                                              P, P, P]),
+    ("cco_route", ctypes.c_int, [P, P, I32, I64, P, I32, P, P, P]),
+    ("cco_route_grad", ctypes.c_int, [P, P, I32, I64, P, P, I32, P, I64, P]),
+    ("cco_group_product", ctypes.c_int, [P, I32, P, I64, P, I32, I32, P, I64, P]),
+    ("cco_group_product_dx", ctypes.c_int, [P, I32, P, I64, P, I32, I32, P, I64, P]),
+    ("cco_group_product_dw", ctypes.c_int, [P, I32, P, I64, P, I64, I32, I32, P, I32, I32, P]),
+    ("cco_block_norm", ctypes.c_int, [P, P, P, I32, P, P, P]),
+    ("cco_block_norm_grad_workspace", U64, [P, I32]),
+    ("cco_block_norm_grad", ctypes.c_int, [P, P, P, P, P, I32, P, P, P, P, P, P, U64, P]),
+    ("cco_moe_combine_norm", ctypes.c_int, [P, P, P, P, I32, P, P, P, P]),
     ("cco_status_string", ctypes.c_char_p, [ctypes.c_int]),
 ]
 

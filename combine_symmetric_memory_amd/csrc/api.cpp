@@ -18,6 +18,7 @@
 
 #include "../../include/cco_moe.h"
 #include "cco_internal.h"
+#include "ops_internal.h"
 
 using cco::MoeArgs;
 
@@ -173,6 +174,28 @@ void free_moe(cco_moe *m) {
 }
 
 }  // namespace
+
+namespace cco {
+
+// What the fused combine of cco_ops.h needs of a layer, with the checks
+// cco_moe_combine makes of its state.
+int moe_combine_view(::cco_moe *m, int32_t T, CombineView *out, int *device, int32_t *hidden) {
+  if (!m || T < 0 || T != m->planned_T) return CCO_ERR_INVALID_ARG;
+  // identity experts would hand the combine the 8-bit receive rows as bf16
+  if (T > 0 && m->shape.inter == 0 && m->disp_8bit) return CCO_ERR_INVALID_ARG;
+  out->moe = m->args;
+  out->win = m->shape.inter > 0 ? m->lay.out_tok : m->lay.disp_x;
+  *device = m->heap->device;
+  *hidden = m->shape.hidden;
+  return CCO_OK;
+}
+
+// `fn(ctx)`, timed as the layer's combine while its timing is on.
+int moe_timed_combine(::cco_moe *m, hipStream_t st, hipError_t (*fn)(void *), void *ctx) {
+  return timed_launch(m, 5, st, [&] { return fn(ctx); });
+}
+
+}  // namespace cco
 
 extern "C" {
 

@@ -1,0 +1,238 @@
+// group.hip -- matrix products over rows grouped by expert, with their
+// gradients (include/cco_ops.h):
+//
+//   product  y[r]  = x[r] W_g^T             rows ragged, both operands k-contiguous
+//   dx       dx[r] = dy[r] W_g              rows ragged, W_g k-major (k here: n)
+//   dw       dW_g  = sum_r dy[r]^T x[r]     reduction ragged, both k-major
+//
+// The general kernel: 128 x 128 tiles on four wavefronts, each 64 x 64 as
+// 2 x 2 blocks of 32x32x16 MFMAs with fp32 sums; reduction steps of 64
+// through two LDS buffers, the next step's operands in registers while the
+// present one is multiplied.  Every global access is checked against its
+// matrix, so any size, row distance and alignment is right.
+#include "group_common.h"
+
+namespace cco {
+namespace {
+
+constexpr int kGenTile = 128, kGenThreads = 256, kGenStep = 64;
+constexpr int kGenOperand = kGenTile * kGenStep * 2;  // bytes of one operand's step
+
+// Eight elements from column c of row r of a [nr][nc] matrix, zeros outside.
+__device__ __forceinline__ u32x4 load8(const char *base, int64_t ld, int64_t r, int c, int64_t nr,
+                                       int nc) {
+  u32x4 v = {0, 0, 0, 0};
+  if (r < nr && c < nc) {
+    const char *p = base + (r * ld + c) * 2;
+    if (c + 8 <= nc) {
+      __builtin_memcpy(&v, p, 16);  // any alignment
+    } else {
+      uint16_t e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        e[i] = 0;
+        if (c + i < nc) __builtin_memcpy(&e[i], p + 2 * i, 2);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (uint32_t)e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
+    }
+  }
+  return v;
+}
+
+// One operand of the tile: a matrix [nr][nc] (a group's part), and where the
+// tile sits in it.  KC: rows row0.. are tile rows, columns are the
+// reduction.  Otherwise rows are the reduction and columns col0.. the tile's.
+template <bool KC>
+struct GenOperand {
+  const char *base;
+  int64_t ld, nr;
+  int32_t nc;
+  int64_t row0;
+  int32_t col0;
+  u32x4 stage[4];
+
+  __device__ __forceinline__ void fetch(int64_t k0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = q * kGenThreads + threadIdx.x;  // chunk of the step
+      if (KC)
+        stage[q] = load8(base, ld, row0 + i / 8, (int)k0 + i % 8 * 8, nr, nc);
+      else
+        stage[q] = load8(base, ld, k0 + i / 16, col0 + i % 16 * 8, nr, nc);
+    }
+  }
+  __device__ __forceinline__ void put(char *lds) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = q * kGenThreads + threadIdx.x;
+      const int at = KC ? (i / 8) * 128 + ((i % 8) ^ swz<8>(i / 8)) * 16
+                        : (i / 16) * 256 + ((i % 16) ^ kswz(i / 16)) * 16;
+      *(u32x4 *)(lds + at) = stage[q];
+    }
+  }
+  // fragment of the 32 tile rows / columns from `at`, sub-step sk
+  __device__ __forceinline__ u32x4 frag(const char *lds, int at, int sk) const {
+    const int lane = threadIdx.x % kWave;
+    const uint32_t b = lds_addr(lds);
+    if (KC) {
+      const int row = at + (lane & 31), c = sk * 2 + (lane >> 5);
+      return *(lds_cu32x4_t *)(uintptr_t)(b + row * 128 + ((c ^ swz<8>(row)) * 16));
+    }
+    const uint32_t p = b + kmajor_offset<kGenTile>(lane, at) + sk * 16 * 256;
+    const u32x2 lo = lds_read_tr(p), hi = lds_read_tr(p + 4 * 256);
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+  }
+};
+
+template <int OP, bool F16, bool OUT32>
+__global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a) {
+  __shared__ __align__(16) char lds[2][2][kGenOperand];
+  constexpr bool AKC = OP != kGroupDw, BKC = OP == kGroupProduct;
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int wm = wave / 2, wn = wave % 2;
+  // output columns, and (dw) output rows
+  const int ncol = OP == kGroupProduct ? a.n : a.k;
+  const int ct = (ncol + kGenTile - 1) / kGenTile;
+  TileMap<kGenThreads> map;
+  map.init(a, (int64_t *)&lds[0][0][0], [&](int rows) {
+    return OP == kGroupDw ? ct * ((a.n + kGenTile - 1) / kGenTile)
+                          : (rows + kGenTile - 1) / kGenTile * ct;
+  });
+  for (int64_t L = blockIdx.x; L < map.total; L += gridDim.x) {
+    int g, r;
+    map.find(L, (int32_t *)&lds[0][0][0], g, r);
+    const GroupRows gr = group_rows(a, g);
+    const int row0 = r / ct * kGenTile, col0 = r % ct * kGenTile;
+    const int64_t welems = (int64_t)a.n * a.k;
+    GenOperand<AKC> oa;
+    GenOperand<BKC> ob;
+    int64_t kdim;       // reduction length
+    int32_t out_rows;   // rows of this group's output
+    oa.base = a.a + gr.lo * a.lda * 2;
+    oa.ld = a.lda;
+    oa.nr = gr.n;
+    oa.nc = OP == kGroupProduct ? a.k : a.n;
+    oa.row0 = oa.col0 = row0;
+    if (OP == kGroupDw) {
+      kdim = gr.n;
+      out_rows = a.n;
+      ob.base = a.b + gr.lo * a.ldb * 2;
+      ob.nr = gr.n;
+    } else {
+      kdim = oa.nc;
+      out_rows = gr.n;
+      ob.base = a.b + (int64_t)g * welems * 2;
+      ob.nr = a.n;
+    }
+    ob.ld = a.ldb;
+    ob.nc = a.k;
+    ob.row0 = ob.col0 = col0;
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    const int64_t steps = (kdim + kGenStep - 1) / kGenStep;
+    if (steps > 0) {
+      oa.fetch(0);
+      ob.fetch(0);
+      oa.put(lds[0][0]);
+      ob.put(lds[0][1]);
+    }
+    __syncthreads();
+    for (int64_t s = 0; s < steps; ++s) {
+      const int cur = (int)(s & 1);
+      if (s + 1 < steps) {
+        oa.fetch((s + 1) * kGenStep);
+        ob.fetch((s + 1) * kGenStep);
+      }
+#pragma unroll
+      for (int sk = 0; sk < 4; ++sk) {
+        u32x4 fa[2], fb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fa[i] = oa.frag(lds[cur][0], wm * 64 + i * 32, sk);
+          fb[i] = ob.frag(lds[cur][1], wn * 64 + i * 32, sk);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16<F16>(fb[j], fa[i], acc[i][j]);
+      }
+      // the other buffer was last read in step s - 1, before its barrier
+      if (s + 1 < steps) {
+        oa.put(lds[cur ^ 1][0]);
+        ob.put(lds[cur ^ 1][1]);
+      }
+      __syncthreads();
+    }
+    char *cbase = a.c + (OP == kGroupDw ? (int64_t)g * welems : gr.lo * a.ldc) * (OUT32 ? 4 : 2);
+    const int64_t ldc = OP == kGroupDw ? a.k : a.ldc;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = row0 + wm * 64 + i * 32 + (lane & 31);
+          const int col = col0 + wn * 64 + j * 32 + q * 8 + (lane >> 5) * 4;
+          if (row >= out_rows) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (col + c >= ncol) continue;
+            char *p = cbase + (row * ldc + col + c) * (OUT32 ? 4 : 2);
+            float v = acc[i][j][4 * q + c];
+            if constexpr (OUT32) {
+              if (a.accumulate) v += *(float *)p;
+              *(float *)p = v;
+            } else {
+              if (a.accumulate) v += from_half_bits<F16>(*(uint16_t *)p);
+              *(uint16_t *)p = to_half_bits<F16>(v);
+            }
+          }
+        }
+  }
+}
+
+// Largest grid: enough workgroups that the hardware's own hand-out levels
+// uneven tiles; the kernels take further tiles in a loop.
+constexpr int64_t kMaxGrid = 4096;
+
+template <int OP, bool F16, bool OUT32>
+hipError_t launch_general(const GroupArgs &a, hipStream_t st) {
+  const int64_t ncol = OP == kGroupProduct ? a.n : a.k;
+  const int64_t ct = (ncol + kGenTile - 1) / kGenTile;
+  int64_t tiles;
+  if (OP == kGroupDw)
+    tiles = (int64_t)a.groups * ct * ((a.n + kGenTile - 1) / kGenTile);
+  else  // every group with rows has at most one partly filled row of tiles
+    tiles = (a.rows / kGenTile + std::min<int64_t>(a.groups, a.rows)) * ct;
+  if (tiles == 0) return hipSuccess;
+  hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32>),
+                     dim3((uint32_t)std::min(tiles, kMaxGrid)), dim3(kGenThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int OP>
+hipError_t launch_op(bool f16, bool out_f32, bool aligned, const GroupArgs &a, hipStream_t st) {
+  if constexpr (OP == kGroupDw)
+    if (out_f32)
+      return f16 ? launch_general<OP, true, true>(a, st) : launch_general<OP, false, true>(a, st);
+  return f16 ? launch_general<OP, true, false>(a, st) : launch_general<OP, false, false>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_group(GroupOp op, bool f16, bool out_f32, bool aligned, const GroupArgs &a,
+                        hipStream_t st) {
+  switch (op) {
+    case kGroupProduct: return launch_op<kGroupProduct>(f16, out_f32, aligned, a, st);
+    case kGroupDx: return launch_op<kGroupDx>(f16, out_f32, aligned, a, st);
+    default: return launch_op<kGroupDw>(f16, out_f32, aligned, a, st);
+  }
+}
+
+}  // namespace cco
