@@ -126,9 +126,15 @@ __device__ __forceinline__ int kswz(int k) { return ((k & 1) ? 4 : 0) ^ ((k & 2)
 
 // ds_read_b64_tr_b16: within 16 lanes, lane s reads 4 columns of k row
 // s / 4; lane l gets column l of the 16 at k 0..3 of the 4 rows.
+// (The restrict pointer gives the read alias information.  Without any, the
+// compiler takes it to depend on every direct load into LDS in flight and
+// waits for all of them before each read; the kernels order the two with
+// explicit waits.)
+__device__ __forceinline__ u32x2 read_tr(lds_s16x4_t *__restrict__ p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
 __device__ __forceinline__ u32x2 lds_read_tr(uint32_t addr) {
-  return __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t *)(uintptr_t)addr));
+  return read_tr((lds_s16x4_t *)(uintptr_t)addr);
 }
 
 // Byte offset in LDS of this lane's fragment reads of 32 columns starting at

@@ -38,8 +38,8 @@ cco::RouteArgs route_args(const cco_route_desc *d, const void *logits, int32_t d
 }
 
 // row distances and widths the kernels address with 31-bit byte offsets
-// inside a 256-row tile
-bool width_ok(int64_t v) { return v >= 1 && v < (1 << 22); }
+// inside a tile of up to 512 rows
+bool width_ok(int64_t v) { return v >= 1 && v < (1 << 21); }
 
 int group_call(cco::GroupOp op, const cco_groups *g, int32_t dtype, const void *a, int64_t lda,
                int32_t acols, const void *b, int64_t ldb, int32_t bcols, int32_t n, int32_t k,

@@ -103,7 +103,7 @@ typedef struct {
  *   dtype  CCO_BF16 or CCO_F16, for x, w and y; sums in fp32
  *   x      [rows][k], row distance ldx;  w  [groups][n][k], dense
  *   y      [rows][n], row distance ldy
- * n, k >= 1, 256 times any row distance and 256 * n, 256 * k below 2^30.
+ * n, k and the row distances lie in [1, 2^21).
  * Rows of whole 16 bytes (n, k and the distances multiples of 8, pointers
  * 16-byte aligned) take the fast kernel, others a general one. */
 int cco_group_product(const cco_groups *g, int32_t dtype, const void *x, int64_t ldx,
