@@ -1,9 +1,9 @@
 // block_norm.hip -- the norms around a block, fused with its gate and
 // residual, and their gradient (include/cco_ops.h).
 //
-//   z = post ? y ry post : y,          ry = rsqrt(mean y^2 + eps)
+//   z = post ? y ry post : y,          ry = 1 / sqrt(mean y^2 + eps)
 //   out = x + scale gate z
-//   u = out ro pre,                    ro = rsqrt(mean out^2 + eps)
+//   u = out ro pre,                    ro = 1 / sqrt(mean out^2 + eps)
 //
 // Gradient, with q = du pre and M = mean(q out):
 //   d  = dout + ro q - out ro^3 M                              (dx)
@@ -12,94 +12,141 @@
 //   dpost = sum_t dz y ry,   dpre = sum_t du out ro
 // mean(b y) would be a third sum over the row that waits for M; it is linear
 // in d, so the row's second sum also carries v . dout, v . q and v . out
-// (v = scale gate post y) and mean(b y) follows from them.
+// (v = scale gate post y) and mean(b y) follows from them.  With
+// C = sum_t scale d y ry (times a token gate), dpost = gate C and a channel's
+// dgate = post C: one column sum serves both.
 //
 // Bound by memory: every row is read once and stays in one workgroup's
-// registers.  Workgroups walk the rows with the vectors post, gate and pre
-// in registers; the gradient's column sums stay in registers too, one
-// partial per workgroup, added in workgroup order by a second kernel (no
-// atomics).
+// registers, 16 elements a thread (8 for rows of at most 512).  Workgroups
+// walk the rows with the vectors in registers and the next row's loads in
+// flight while the present one is summed; as many workgroups as the
+// registers let run at once.  The gradient's column sums stay in registers
+// too, one partial per workgroup, added in workgroup order by a second
+// kernel (no atomics).
 #include "combine_impl.h"
 #include "ops_internal.h"
 
 namespace cco {
 namespace {
 
-template <int DT>
-struct Elem;
-template <>
-struct Elem<CCO_BF16> {
-  typedef __bf16 T;
-};
-template <>
-struct Elem<CCO_F16> {
-  typedef _Float16 T;
-};
-template <>
-struct Elem<CCO_F32> {
-  typedef float T;
+constexpr int kNumCus = 256;
+
+// Eight elements as they lie in memory (16-bit types 16 bytes, fp32 32).
+// Rows and vectors may be aligned to an element only: the loads are
+// unaligned 16-byte ones, which cost nothing where the address is aligned.
+template <class T>
+struct Raw8 {
+  T v[8];
 };
 
-// A thread's share of a row: NV vectors of VW elements.  VW 8: the row is
-// whole 16-byte vectors, vector i of thread t is vector i * threads + t;
-// VW 1: single elements (any width, any alignment).
-template <class T, int VW>
-__device__ __forceinline__ void load_vec(const T *p, float *v) {
-  if constexpr (VW == 1) {
-    v[0] = (float)p[0];
-  } else if constexpr (sizeof(T) == 2) {
-    typedef T t8 __attribute__((ext_vector_type(8)));
-    const t8 q = *(const t8 *)p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)q[i];
+// Elements [at, at + 8) of a row of H, zeros past its end.
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T *row, int at, int H) {
+  Raw8<T> r;
+  if (at + 8 <= H) {
+    __builtin_memcpy(&r, row + at, sizeof(r));
   } else {
-    typedef float f4 __attribute__((ext_vector_type(4)));
-    const f4 a = ((const f4 *)p)[0], b = ((const f4 *)p)[1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
+    for (int c = 0; c < 8; ++c) r.v[c] = at + c < H ? row[at + c] : (T)0.0f;
+  }
+  return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store8(T *row, int at, int H, const float *v) {
+  Raw8<T> r;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) r.v[c] = (T)v[c];
+  if (at + 8 <= H) {
+    __builtin_memcpy(row + at, &r, sizeof(r));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (at + c < H) row[at + c] = r.v[c];
+  }
+}
+
+// A thread's share of a row: NV vectors, vector i at (i * threads + t) * 8.
+template <class T, int NV>
+struct RowRaw {
+  Raw8<T> v[NV];
+  __device__ __forceinline__ void load(const T *row, int H) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = load8(row, (i * blockDim.x + threadIdx.x) * 8, H);
+  }
+  __device__ __forceinline__ void get(float (&f)[NV * 8]) const {
+#pragma unroll
+    for (int i = 0; i < NV * 8; ++i) f[i] = (float)v[i / 8].v[i % 8];
+  }
+};
+
+template <class T, int NV>
+__device__ __forceinline__ void store_row(T *row, int H, const float (&v)[NV * 8]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    store8(row, (i * blockDim.x + threadIdx.x) * 8, H, v + i * 8);
+}
+
+// A parameter vector's elements of this thread (1 where absent).
+template <class T, int NV>
+__device__ __forceinline__ void load_param(const void *p, int f32, int H, float (&v)[NV * 8]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = (i * blockDim.x + threadIdx.x) * 8;
+    if (!p) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[i * 8 + c] = 1.0f;
+    } else if (f32) {
+      const Raw8<float> r = load8((const float *)p, at, H);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[i * 8 + c] = r.v[c];
+    } else {
+      const Raw8<T> r = load8((const T *)p, at, H);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[i * 8 + c] = (float)r.v[c];
     }
   }
 }
 
-template <class T, int VW>
-__device__ __forceinline__ void store_vec(T *p, const float *v) {
-  if constexpr (VW == 1) {
-    p[0] = (T)v[0];
-  } else if constexpr (sizeof(T) == 2) {
-    typedef T t8 __attribute__((ext_vector_type(8)));
-    t8 q;
+// gate * post of this thread's elements.
+template <class T, int NV>
+__device__ __forceinline__ void load_gate_post(const NormArgs &a, float (&v)[NV * 8]) {
+  float g[NV * 8];
+  load_param<T, NV>(a.post, a.w_f32, a.H, v);
+  load_param<T, NV>(a.gate_kind == CCO_GATE_CHANNEL ? a.gate : nullptr, a.w_f32, a.H, g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = (T)v[i];
-    *(t8 *)p = q;
-  } else {
-    typedef float f4 __attribute__((ext_vector_type(4)));
-    f4 a, b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = v[i];
-      b[i] = v[4 + i];
-    }
-    ((f4 *)p)[0] = a;
-    ((f4 *)p)[1] = b;
-  }
+  for (int i = 0; i < NV * 8; ++i) v[i] *= g[i];
 }
 
-__device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
+                                                               0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+// Sum over the wavefront, the same in every lane: pairs, quads, halves of 16
+// and 16 lanes by data-parallel moves, then the four rows of 16 in order.
+__device__ __forceinline__ float wave_total(float v) {
+  v += dpp<0xB1>(v);   // quad_perm 1 0 3 2
+  v += dpp<0x4E>(v);   // quad_perm 2 3 0 1
+  v += dpp<0x141>(v);  // mirror within 8
+  v += dpp<0x140>(v);  // mirror within 16
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
 
-// Sums of N values over the workgroup (every thread gets them, in the same
-// order of addition).  `buf` alternates between two halves, so one barrier
-// per sum is enough: a half is written again only after the next barrier.
-constexpr int kMaxSums = 5;
+// Sums of N values over the workgroup (every thread gets them, in one order
+// of addition).  `half` alternates between two halves of the scratch, so one
+// barrier per sum is enough: a half is written again only after the next
+// barrier.
+constexpr int kMaxSums = 8, kMaxWaves = 16;
 template <int N>
 __device__ __forceinline__ void block_sum(float (&s)[N], float *lds, int &half, int waves) {
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], d, kWave);
+  for (int i = 0; i < N; ++i) s[i] = wave_total(s[i]);
   if (waves > 1) {
-    float *b = lds + half * (16 * kMaxSums);
+    float *b = lds + half * (kMaxWaves * kMaxSums);
     half ^= 1;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     if (lane == 0)
@@ -114,53 +161,20 @@ __device__ __forceinline__ void block_sum(float (&s)[N], float *lds, int &half, 
   }
 }
 
-// Parameter vectors of a thread's elements (1 where absent).
-template <class T, int VW, int NV>
-__device__ __forceinline__ void load_param(const void *p, int f32, int H, float (&v)[NV * VW]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int at = (i * blockDim.x + threadIdx.x) * VW;
-#pragma unroll
-    for (int c = 0; c < VW; ++c) v[i * VW + c] = 1.0f;
-    if (p && at < H) {
-      // the vectors are aligned to an element only
-#pragma unroll
-      for (int c = 0; c < VW; ++c)
-        v[i * VW + c] = f32 ? ((const float *)p)[at + c] : (float)((const T *)p)[at + c];
-    }
-  }
-}
-
-template <class T, int VW, int NV>
-__device__ __forceinline__ void load_row(const T *row, int H, float (&v)[NV * VW]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int at = (i * blockDim.x + threadIdx.x) * VW;
-#pragma unroll
-    for (int c = 0; c < VW; ++c) v[i * VW + c] = 0.0f;
-    if (row && at < H) load_vec<T, VW>(row + at, v + i * VW);
-  }
-}
-
-template <class T, int VW, int NV>
-__device__ __forceinline__ void store_row(T *row, int H, const float (&v)[NV * VW]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int at = (i * blockDim.x + threadIdx.x) * VW;
-    if (at < H) store_vec<T, VW>(row + at, v + i * VW);
-  }
-}
-
 __device__ __forceinline__ float rms_inverse(float sum, int H, float eps) {
   return 1.0f / sqrtf(sum / (float)H + eps);
 }
 
+__device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // A thread's share of combine's output row of token t, rounded to bf16: the
-// sum over the token's K pairs in order, as combine_token forms it.
+// sum over the token's K pairs in order, as combine_token forms it.  (H is a
+// multiple of 8 and the windows are aligned.)
 template <int NV>
 __device__ __forceinline__ void combine_row(const CombineView &c, int t, int H,
-                                            float (&y)[NV * 8]) {
+                                            RowRaw<__bf16, NV> &out) {
   const MoeArgs &a = c.moe;
+  float y[NV * 8];
 #pragma unroll
   for (int i = 0; i < NV * 8; ++i) y[i] = 0.0f;
   constexpr int B = 8;  // pairs whose rows are in flight together
@@ -202,104 +216,141 @@ __device__ __forceinline__ void combine_row(const CombineView &c, int t, int H,
             }
   }
 #pragma unroll
-  for (int i = 0; i < NV * 8; ++i) y[i] = (float)(__bf16)y[i];
+  for (int i = 0; i < NV * 8; ++i) out.v[i / 8].v[i % 8] = (__bf16)y[i];
 }
 
-template <class T, int VW, int NV, bool COMBINE>
+template <class T, int NV, bool COMBINE>
 __device__ __forceinline__ void norm_rows(const NormArgs &a, const CombineView *cv) {
-  constexpr int N = NV * VW;
-  __shared__ float lds[2 * 16 * kMaxSums];
+  constexpr int N = NV * 8;
+  __shared__ float lds[2 * kMaxWaves * kMaxSums];
   int half = 0;
   const int waves = blockDim.x / kWave, H = a.H;
-  float gate[N], post[N], pre[N];
-  load_param<T, VW, NV>(a.gate_kind == CCO_GATE_CHANNEL ? a.gate : nullptr, a.w_f32, H, gate);
-  load_param<T, VW, NV>(a.post, a.w_f32, H, post);
-  load_param<T, VW, NV>(a.pre, a.w_f32, H, pre);
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  const bool has_y = COMBINE || a.y;
+  RowRaw<T, NV> rx, ry;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    rx.load((const T *)a.x + (int64_t)t * H, H);
+    if constexpr (!COMBINE)
+      if (has_y) ry.load((const T *)a.y + (int64_t)t * H, H);
+  };
+  int t = blockIdx.x;
+  fetch(t);
+  float gp[N], pre[N];
+  load_gate_post<T, NV>(a, gp);
+  load_param<T, NV>(a.pre, a.w_f32, H, pre);
+  for (; t < a.T; t += gridDim.x) {
     const int64_t off = (int64_t)t * H;
     float o[N], y[N];
-    load_row<T, VW, NV>((const T *)a.x + off, H, o);
-    if (COMBINE || a.y) {
-      if constexpr (COMBINE) {
-        combine_row<NV>(*cv, t, H, y);
-        if (cv->y_out) store_row<T, VW, NV>((T *)cv->y_out + off, H, y);
-      } else {
-        load_row<T, VW, NV>((const T *)a.y + off, H, y);
+    if constexpr (COMBINE) {
+      combine_row<NV>(*cv, t, H, ry);
+      if (cv->y_out) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int at = (i * blockDim.x + threadIdx.x) * 8;
+          if (at < H) *(Raw8<T> *)((T *)cv->y_out + off + at) = ry.v[i];
+        }
       }
+    }
+    rx.get(o);
+    if (has_y) ry.get(y);
+    if (t + (int)gridDim.x < a.T) fetch(t + gridDim.x);
+    if (has_y) {
       float s = a.scale;
       if (a.gate_kind == CCO_GATE_TOKEN) s *= ((const float *)a.gate)[t];
-      float ry[1] = {1.0f};
       if (a.post) {
-        ry[0] = 0.0f;
+        float sum[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < N; ++i) ry[0] = __builtin_fmaf(y[i], y[i], ry[0]);
-        block_sum<1>(ry, lds, half, waves);
-        ry[0] = rms_inverse(ry[0], H, a.eps);
+        for (int i = 0; i < N; ++i) sum[0] = __builtin_fmaf(y[i], y[i], sum[0]);
+        block_sum<1>(sum, lds, half, waves);
+        s *= rms_inverse(sum[0], H, a.eps);
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(s * gate[i], y[i] * ry[0] * post[i], o[i]);
-      if (a.out) store_row<T, VW, NV>((T *)a.out + off, H, o);
+      for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(s * gp[i], y[i], o[i]);
+      if (a.out) store_row<T, NV>((T *)a.out + off, H, o);
     }
     if (a.u) {
-      float ro[1] = {0.0f};
+      float sum[1] = {0.0f};
 #pragma unroll
-      for (int i = 0; i < N; ++i) ro[0] = __builtin_fmaf(o[i], o[i], ro[0]);
-      block_sum<1>(ro, lds, half, waves);
-      const float r = rms_inverse(ro[0], H, a.eps);
+      for (int i = 0; i < N; ++i) sum[0] = __builtin_fmaf(o[i], o[i], sum[0]);
+      block_sum<1>(sum, lds, half, waves);
+      const float r = rms_inverse(sum[0], H, a.eps);
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i] = o[i] * r * pre[i];
-      store_row<T, VW, NV>((T *)a.u + off, H, o);
+      store_row<T, NV>((T *)a.u + off, H, o);
     }
   }
 }
 
-template <class T, int VW, int NV>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
-  norm_rows<T, VW, NV, false>(a, nullptr);
+template <class T, int NV, int MAXT>
+__global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs a) {
+  norm_rows<T, NV, false>(a, nullptr);
 }
 
-template <int NV>
-__global__ __launch_bounds__(1024) void combine_norm_kernel(CombineView c, NormArgs a) {
-  norm_rows<__bf16, 8, NV, true>(a, &c);
+template <int NV, int MAXT>
+__global__ __launch_bounds__(MAXT) void combine_norm_kernel(CombineView c, NormArgs a) {
+  norm_rows<__bf16, NV, true>(a, &c);
 }
 
-template <class T, int VW, int NV>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
-  constexpr int N = NV * VW;
-  __shared__ float lds[2 * 16 * kMaxSums];
+// KEEP: the vectors stay in registers and the next row is fetched ahead;
+// otherwise (rows of more than 512 threads, whose register budget is half)
+// both are read when they are needed.
+template <class T, int NV, int MAXT, bool KEEP>
+__global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
+  constexpr int N = NV * 8;
+  __shared__ float lds[2 * kMaxWaves * kMaxSums];
   int half = 0;
   const int waves = blockDim.x / kWave, H = a.H;
   const float inv_h = 1.0f / (float)H;
-  const bool channel = a.gate_kind == CCO_GATE_CHANNEL, token = a.gate_kind == CCO_GATE_TOKEN;
-  float gate[N], post[N], pre[N], dgate[N], dpost[N], dpre[N];
-  load_param<T, VW, NV>(channel ? a.gate : nullptr, a.w_f32, H, gate);
-  load_param<T, VW, NV>(a.post, a.w_f32, H, post);
-  load_param<T, VW, NV>(a.pre, a.w_f32, H, pre);
+  const bool token = a.gate_kind == CCO_GATE_TOKEN;
+  RowRaw<T, NV> rx, ry, rd, rq;
 #pragma unroll
-  for (int i = 0; i < N; ++i) dgate[i] = dpost[i] = dpre[i] = 0.0f;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int i = 0; i < N; ++i)
+    ry.v[i / 8].v[i % 8] = rd.v[i / 8].v[i % 8] = rq.v[i / 8].v[i % 8] = (T)0.0f;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    const int64_t off = (int64_t)t * H;
+    if (a.y) ry.load((const T *)a.y + off, H);
+    rx.load((const T *)a.x + off, H);
+    if (a.dout) rd.load((const T *)a.dout + off, H);
+    if (a.du) rq.load((const T *)a.du + off, H);
+  };
+  int t = blockIdx.x;
+  if (KEEP) fetch(t);
+  float gp[N], pre[N], csum[N], dpre[N];
+  if (KEEP) {
+    load_gate_post<T, NV>(a, gp);
+    load_param<T, NV>(a.pre, a.w_f32, H, pre);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) csum[i] = dpre[i] = 0.0f;
+  for (; t < a.T; t += gridDim.x) {
     const int64_t off = (int64_t)t * H;
     float x[N], y[N], d[N], q[N];
-    load_row<T, VW, NV>((const T *)a.x + off, H, x);
-    load_row<T, VW, NV>(a.y ? (const T *)a.y + off : nullptr, H, y);
-    load_row<T, VW, NV>(a.dout ? (const T *)a.dout + off : nullptr, H, d);
-    load_row<T, VW, NV>(a.du ? (const T *)a.du + off : nullptr, H, q);
+    if (!KEEP) {
+      fetch(t);
+      load_gate_post<T, NV>(a, gp);
+      load_param<T, NV>(a.pre, a.w_f32, H, pre);
+    }
+    rx.get(x);
+    ry.get(y);
+    rd.get(d);
+    rq.get(q);
+    if (KEEP && t + (int)gridDim.x < a.T) fetch(t + gridDim.x);
     const float tg = token ? ((const float *)a.gate)[t] : 1.0f;
-    float ry = 1.0f;
+    float ry1 = 1.0f;
     if (a.post) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < N; ++i) s[0] = __builtin_fmaf(y[i], y[i], s[0]);
       block_sum<1>(s, lds, half, waves);
-      ry = rms_inverse(s[0], H, a.eps);
+      ry1 = rms_inverse(s[0], H, a.eps);
     }
     const float st = a.scale * tg;
-    // x becomes out; v = scale gate_channel post y
+    // x becomes out, q becomes du pre; v = gate_channel post y
     float s[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    const float sry = st * ry1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = __builtin_fmaf(st * gate[i], y[i] * ry * post[i], x[i]);
-      const float v = a.scale * gate[i] * post[i] * y[i], qi = q[i] * pre[i];
+      const float v = gp[i] * y[i], qi = q[i] * pre[i];
+      x[i] = __builtin_fmaf(sry, v, x[i]);
       s[0] = __builtin_fmaf(x[i], x[i], s[0]);
       s[1] = __builtin_fmaf(qi, x[i], s[1]);
       s[2] = __builtin_fmaf(v, d[i], s[2]);
@@ -308,127 +359,115 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormArgs a) {
     }
     block_sum<5>(s, lds, half, waves);
     const float ro = a.pre ? rms_inverse(s[0], H, a.eps) : 0.0f;
-    const float m3 = ro * ro * ro * s[1] * inv_h;                   // ro^3 M
-    const float vd = s[2] + ro * s[3] - m3 * s[4];                  // v . d
-    if (token && threadIdx.x == 0) a.dgate[t] = vd * ry;
-    const float by = a.post ? ry * ry * ry * tg * vd * inv_h : 0.0f;  // ry^3 mean(b y)
+    const float m3 = ro * ro * ro * s[1] * inv_h;               // ro^3 M
+    const float vd = a.scale * (s[2] + ro * s[3] - m3 * s[4]);  // scale v . d
+    if (token && threadIdx.x == 0) a.dgate[t] = vd * ry1;
+    const float by = a.post ? ry1 * ry1 * ry1 * tg * vd * inv_h : 0.0f;  // ry^3 mean(b y)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      dpre[i] = __builtin_fmaf(q[i], x[i] * ro, dpre[i]);
+      dpre[i] = __builtin_fmaf(q[i] * ro, x[i], dpre[i]);
       d[i] += ro * (q[i] * pre[i]) - x[i] * m3;
-      const float yr = y[i] * ry;
-      const float sd = a.scale * d[i];
-      dgate[i] = __builtin_fmaf(sd, yr * post[i], dgate[i]);
-      const float dz = sd * tg * gate[i];
-      dpost[i] = __builtin_fmaf(dz, yr, dpost[i]);
-      q[i] = __builtin_fmaf(-y[i], by, ry * (dz * post[i]));
+      const float sd = sry * d[i];
+      csum[i] = __builtin_fmaf(sd, y[i], csum[i]);
+      q[i] = __builtin_fmaf(-y[i], by, sd * gp[i]);
     }
-    store_row<T, VW, NV>((T *)a.dx + off, H, d);
-    if (a.dy) store_row<T, VW, NV>((T *)a.dy + off, H, q);
+    store_row<T, NV>((T *)a.dx + off, H, d);
+    if (a.dy) store_row<T, NV>((T *)a.dy + off, H, q);
   }
-  // this workgroup's column sums: [sum kind][workgroup][H]
+  // this workgroup's column sums: [sum][workgroup][H]
   float *part = a.partial + (int64_t)blockIdx.x * H;
-  const int64_t kind = (int64_t)gridDim.x * H;
-  auto leave = [&](const float (&v)[N]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = (i * blockDim.x + threadIdx.x) * VW;
-      if (at < H)
-#pragma unroll
-        for (int c = 0; c < VW; ++c) part[at + c] = v[i * VW + c];
-    }
-    part += kind;
-  };
-  if (a.dpost) leave(dpost);
-  if (channel) leave(dgate);
-  if (a.dpre) leave(dpre);
+  if (a.dpost || a.gate_kind == CCO_GATE_CHANNEL) {
+    store_row<float, NV>(part, H, csum);
+    part += (int64_t)gridDim.x * H;
+  }
+  if (a.dpre) store_row<float, NV>(part, H, dpre);
 }
 
-// out[h] = sum over the workgroups of partial[w][h], in fixed order: 16
-// chains of every 16th workgroup, then the chains in order.
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float *partial, int nwg, int H,
-                                                          float *o0, float *o1, float *o2) {
+// Columns of the partial sums, added in fixed order: 16 chains of every 16th
+// workgroup, then the chains in order.  Block y 0 is C (where it exists),
+// the other dpre.
+__global__ __launch_bounds__(1024) void column_sum_kernel(NormArgs a, int nwg) {
   __shared__ float lds[16][kWave];
-  float *outs[3] = {o0, o1, o2};
-  const float *part = partial + (int64_t)blockIdx.y * nwg * H;
+  const bool has_c = a.dpost || a.gate_kind == CCO_GATE_CHANNEL;
+  const float *part = a.partial + (int64_t)blockIdx.y * nwg * a.H;
   const int lane = threadIdx.x % kWave, chain = threadIdx.x / kWave;
   const int h = blockIdx.x * kWave + lane;
   float s = 0.0f;
-  if (h < H)
-    for (int w = chain; w < nwg; w += 16) s += part[(int64_t)w * H + h];
+  if (h < a.H)
+    for (int w = chain; w < nwg; w += 16) s += part[(int64_t)w * a.H + h];
   lds[chain][lane] = s;
   __syncthreads();
-  if (chain == 0 && h < H) {
-    for (int c = 1; c < 16; ++c) s += lds[c][lane];
-    float *o = blockIdx.y == 0 ? o0 : (blockIdx.y == 1 ? o1 : o2);
-    o[h] = s;
+  if (chain != 0 || h >= a.H) return;
+  for (int c = 1; c < 16; ++c) s += lds[c][lane];
+  if (!has_c || blockIdx.y == 1) {
+    a.dpre[h] = s;
+    return;
   }
+  auto param = [&](const void *p) -> float {
+    if (!p) return 1.0f;
+    return a.w_f32 ? ((const float *)p)[h] : (a.w_f16 ? (float)((const _Float16 *)p)[h]
+                                                      : (float)((const __bf16 *)p)[h]);
+  };
+  const bool channel = a.gate_kind == CCO_GATE_CHANNEL;
+  if (a.dpost) a.dpost[h] = s * param(channel ? a.gate : nullptr);
+  if (channel) a.dgate[h] = s * param(a.post);
 }
 
-// Threads per row for n vectors with NV vectors each.
-int row_threads(int n, int nv) { return ((n + nv - 1) / nv + kWave - 1) / kWave * kWave; }
-
-bool all_aligned16(std::initializer_list<const void *> ps) {
-  for (const void *p : ps)
-    if ((uintptr_t)p & 15) return false;
-  return true;
+// Vectors per thread and threads per row.
+struct RowShape {
+  int nv, threads;
+};
+RowShape row_shape(int H) {
+  const int nv = H <= 512 ? 1 : 2;
+  const int n = (H + 7) / 8;
+  return {nv, ((n + nv - 1) / nv + kWave - 1) / kWave * kWave};
+}
+// Workgroups that fill the chip with `per_cu` threads a CU.
+int row_grid(int64_t T, int threads, int per_cu) {
+  return (int)std::min<int64_t>(T, (int64_t)kNumCus * std::max(1, per_cu / threads));
 }
 
 template <class T>
 hipError_t launch_norm(const NormArgs &a, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  const int H = a.H;
-  const int grid = a.T < 2048 ? a.T : 2048;
-  const bool vec = H % 8 == 0 && all_aligned16({a.x, a.y, a.out, a.u});
-  auto go = [&](auto kernel, int nvec, int nv) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(row_threads(nvec, nv)), 0, st, a);
-    return hipGetLastError();
-  };
-  if (vec) return H <= 8192 ? go(norm_kernel<T, 8, 1>, H / 8, 1) : go(norm_kernel<T, 8, 2>, H / 8, 2);
-  if (H <= 1024) return go(norm_kernel<T, 1, 1>, H, 1);
-  if (H <= 4096) return go(norm_kernel<T, 1, 4>, H, 4);
-  if (H <= 8192) return go(norm_kernel<T, 1, 8>, H, 8);
-  return go(norm_kernel<T, 1, 16>, H, 16);
+  const RowShape rs = row_shape(a.H);
+  const dim3 grid(row_grid(a.T, rs.threads, 1024)), block(rs.threads);
+  if (rs.nv == 1)
+    hipLaunchKernelGGL((norm_kernel<T, 1, 512>), grid, block, 0, st, a);
+  else if (rs.threads <= 512)
+    hipLaunchKernelGGL((norm_kernel<T, 2, 512>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<T, 2, 1024>), grid, block, 0, st, a);
+  return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_grad(const NormArgs &a, hipStream_t st) {
-  const int H = a.H;
-  const int grid = norm_grad_workgroups(a.T);
-  const bool vec = H % 8 == 0 && all_aligned16({a.x, a.y, a.dout, a.du, a.dx, a.dy});
-  auto go = [&](auto kernel, int nvec, int nv) {
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(row_threads(nvec, nv)), 0, st, a);
-    return hipGetLastError();
-  };
-  hipError_t err = hipSuccess;
-  if (grid > 0) {
-    if (vec)
-      err = H <= 8192 ? go(norm_grad_kernel<T, 8, 1>, H / 8, 1) : go(norm_grad_kernel<T, 8, 2>, H / 8, 2);
-    else if (H <= 1024)
-      err = go(norm_grad_kernel<T, 1, 1>, H, 1);
-    else if (H <= 4096)
-      err = go(norm_grad_kernel<T, 1, 4>, H, 4);
-    else if (H <= 8192)
-      err = go(norm_grad_kernel<T, 1, 8>, H, 8);
+  const RowShape rs = row_shape(a.H);
+  const int nwg = norm_grad_workgroups(a.H, a.T);
+  if (nwg > 0) {
+    const dim3 grid(nwg), block(rs.threads);
+    if (rs.nv == 1)
+      hipLaunchKernelGGL((norm_grad_kernel<T, 1, 512, true>), grid, block, 0, st, a);
+    else if (rs.threads <= 512)
+      hipLaunchKernelGGL((norm_grad_kernel<T, 2, 512, true>), grid, block, 0, st, a);
     else
-      err = go(norm_grad_kernel<T, 1, 16>, H, 16);
+      hipLaunchKernelGGL((norm_grad_kernel<T, 2, 1024, false>), grid, block, 0, st, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
   }
-  if (err != hipSuccess) return err;
-  float *outs[3];
-  int n = 0;
-  if (a.dpost) outs[n++] = a.dpost;
-  if (a.gate_kind == CCO_GATE_CHANNEL) outs[n++] = a.dgate;
-  if (a.dpre) outs[n++] = a.dpre;
-  if (n == 0) return hipSuccess;
-  for (int i = n; i < 3; ++i) outs[i] = outs[0];
-  hipLaunchKernelGGL(column_sum_kernel, dim3((H + kWave - 1) / kWave, n), dim3(1024), 0, st,
-                     a.partial, grid, H, outs[0], outs[1], outs[2]);
+  const int sums = (a.dpost || a.gate_kind == CCO_GATE_CHANNEL) + (a.dpre != nullptr);
+  if (sums == 0) return hipSuccess;
+  hipLaunchKernelGGL(column_sum_kernel, dim3((a.H + kWave - 1) / kWave, sums), dim3(1024), 0, st,
+                     a, nwg);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int norm_grad_workgroups(int32_t T) { return T < 256 ? T : 256; }
+int norm_grad_workgroups(int32_t H, int32_t T) {
+  return row_grid(T, row_shape(H).threads, 512);
+}
 
 hipError_t launch_block_norm(int dtype, const NormArgs &a, hipStream_t st) {
   switch (dtype) {
@@ -448,11 +487,14 @@ hipError_t launch_block_norm_grad(int dtype, const NormArgs &a, hipStream_t st) 
 
 hipError_t launch_combine_norm(const CombineView &c, const NormArgs &a, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  const int grid = a.T < 2048 ? a.T : 2048, nvec = a.H / 8;
-  if (a.H <= 8192)
-    hipLaunchKernelGGL((combine_norm_kernel<1>), dim3(grid), dim3(row_threads(nvec, 1)), 0, st, c, a);
+  const RowShape rs = row_shape(a.H);
+  const dim3 grid(row_grid(a.T, rs.threads, 1024)), block(rs.threads);
+  if (rs.nv == 1)
+    hipLaunchKernelGGL((combine_norm_kernel<1, 512>), grid, block, 0, st, c, a);
+  else if (rs.threads <= 512)
+    hipLaunchKernelGGL((combine_norm_kernel<2, 512>), grid, block, 0, st, c, a);
   else
-    hipLaunchKernelGGL((combine_norm_kernel<2>), dim3(grid), dim3(row_threads(nvec, 2)), 0, st, c, a);
+    hipLaunchKernelGGL((combine_norm_kernel<2, 1024>), grid, block, 0, st, c, a);
   return hipGetLastError();
 }
 

@@ -101,6 +101,7 @@ cco::NormArgs norm_args(const cco_block_norm_desc *d, const void *x, const void 
   a.H = d->hidden;
   a.T = T;
   a.w_f32 = d->wdtype == CCO_F32;
+  a.w_f16 = d->wdtype == CCO_F16;
   a.gate_kind = d->gate_kind;
   a.scale = d->scale;
   a.eps = d->eps;
@@ -208,9 +209,9 @@ int cco_block_norm(const cco_block_norm_desc *d, const void *x, const void *y, i
 
 uint64_t cco_block_norm_grad_workspace(const cco_block_norm_desc *d, int32_t T) {
   if (!norm_ok(d, T)) return 0;
-  const uint64_t sums = (d->post != nullptr) + (d->gate_kind == CCO_GATE_CHANNEL) +
-                        (d->pre != nullptr);
-  return sums * (uint64_t)cco::norm_grad_workgroups(T) * (uint64_t)d->hidden * sizeof(float);
+  const uint64_t sums = (d->post || d->gate_kind == CCO_GATE_CHANNEL) + (d->pre != nullptr);
+  return sums * (uint64_t)cco::norm_grad_workgroups(d->hidden, T) * (uint64_t)d->hidden *
+         sizeof(float);
 }
 
 int cco_block_norm_grad(const cco_block_norm_desc *d, const void *x, const void *y,

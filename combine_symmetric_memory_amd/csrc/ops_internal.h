@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/cco_ops.h"
 #include "cco_internal.h"
 
@@ -54,7 +56,8 @@ hipError_t launch_group(GroupOp op, bool f16, bool out_f32, bool aligned, const 
 // -------------------------------------------------------------- the norms
 struct NormArgs {
   int32_t H, T;
-  int32_t w_f32;       // post, pre and a channel gate are fp32 (else the rows' type)
+  int32_t w_f32;       // post, pre and a channel gate are fp32, or the rows' type:
+  int32_t w_f16;       // ... fp16 (else bf16)
   int32_t gate_kind;
   float scale, eps;
   const void *post, *gate, *pre;
@@ -64,7 +67,7 @@ struct NormArgs {
   float *dpost, *dgate, *dpre, *partial;
 };
 // Workgroups of the gradient's row pass, and the column sums each leaves.
-int norm_grad_workgroups(int32_t T);
+int norm_grad_workgroups(int32_t H, int32_t T);
 hipError_t launch_block_norm(int dtype, const NormArgs &a, hipStream_t st);
 hipError_t launch_block_norm_grad(int dtype, const NormArgs &a, hipStream_t st);
 // The combine's view of one layer for the fused form.

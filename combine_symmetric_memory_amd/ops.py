@@ -16,52 +16,48 @@ unless `stream` is given; outputs that are not passed are made by torch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
 
 from . import _capi
 from ._capi import check, lib
-from .moe import MoE, _stream
+from .moe import MoE
 
 _DTYPES = {torch.bfloat16: _capi.CCO_BF16, torch.float16: _capi.CCO_F16,
            torch.float32: _capi.CCO_F32}
 _SCORES = {"softmax": _capi.CCO_SCORE_SOFTMAX, "sigmoid": _capi.CCO_SCORE_SIGMOID}
 
 
-class _On:
-    """The tensors' device made current, and the stream a call runs on.
+class _Elsewhere:
+    """The tensors' device made current, and the stream of a call too, so
+    that memory torch makes for the call belongs to that stream.  A call on
+    torch's current stream of the current device does without."""
 
-    Memory torch makes for a call on a stream that is not torch's current
-    one is made under that stream, so that torch does not hand it to others
-    while the call still uses it."""
-
-    def __init__(self, device: torch.device, stream):
-        self._dev = None
-        if device.index != torch.cuda.current_device():
-            self._dev = torch.cuda.device(device)
-        self._arg = stream
-        self._ctx = None
+    def __init__(self, dev: torch.device, stream):
+        self._stack = contextlib.ExitStack()
+        self._dev, self._stream = dev, stream
 
     def __enter__(self):
-        if self._dev is not None:
-            self._dev.__enter__()
-        if self._arg is None:
-            self.ptr = _stream(None)
-        else:
-            self.ptr = _stream(self._arg)
-            s = self._arg
+        self._stack.enter_context(torch.cuda.device(self._dev))
+        s = self._stream
+        if s is not None:
             if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s)) if int(s) else torch.cuda.default_stream()
-            self._ctx = torch.cuda.stream(s)
-            self._ctx.__enter__()
-        return self
+                s = int(s)
+                s = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+            self._stack.enter_context(torch.cuda.stream(s))
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        if self._dev is not None:
-            self._dev.__exit__(*exc)
+        return self._stack.__exit__(*exc)
+
+
+def _away(dev: torch.device, stream) -> bool:
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+def _current() -> int:
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _dtype(t: torch.Tensor, name: str, allowed=None) -> int:
@@ -83,7 +79,7 @@ def _same(t: torch.Tensor | None, dev: torch.device, name: str, shape=None, dtyp
         return
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError("%s must be a tensor on %s" % (name, dev))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -131,22 +127,25 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renorm: bo
     MoE.plan and MoE.dispatch.  logits [T, E] bf16, fp16 or fp32 with
     contiguous rows; bias fp32 [E]."""
     dev = _device(logits, "logits")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return route(logits, topk, score=score, renorm=renorm, scale=scale, bias=bias,
+                         groups=groups, kept=kept, idx=idx, w=w)
     ld = _rows(logits, dev, "logits")
     code = _dtype(logits, "logits")
     T, E = logits.shape
     _same(bias, dev, "bias", (E,), torch.float32)
     d = _route_desc(E, topk, score, renorm, scale, groups, kept)
-    with _On(dev, stream) as on:
-        if idx is None:
-            idx = torch.empty((T, max(0, int(topk))), dtype=torch.int32, device=dev)
-        else:
-            _same(idx, dev, "idx", (T, topk), torch.int32)
-        if w is None:
-            w = torch.empty((T, max(0, int(topk))), dtype=torch.float32, device=dev)
-        else:
-            _same(w, dev, "w", (T, topk), torch.float32)
-        check(lib.cco_route(ctypes.byref(d), logits.data_ptr(), code, ld, _p(bias), T,
-                            idx.data_ptr(), w.data_ptr(), on.ptr), "cco_route")
+    if idx is None:
+        idx = torch.empty((T, max(0, int(topk))), dtype=torch.int32, device=dev)
+    else:
+        _same(idx, dev, "idx", (T, topk), torch.int32)
+    if w is None:
+        w = torch.empty((T, max(0, int(topk))), dtype=torch.float32, device=dev)
+    else:
+        _same(w, dev, "w", (T, topk), torch.float32)
+    check(lib.cco_route(ctypes.byref(d), logits.data_ptr(), code, ld, _p(bias), T,
+                        idx.data_ptr(), w.data_ptr(), _current()), "cco_route")
     return idx, w
 
 
@@ -156,6 +155,9 @@ def route_grad(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, *,
     """cco_route_grad -> dlogits [T, E] of the logits' type, given dw fp32
     [T, K], the gradient to the weights of the experts idx int32 [T, K]."""
     dev = _device(logits, "logits")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return route_grad(logits, idx, dw, score=score, renorm=renorm, scale=scale, out=out)
     ld = _rows(logits, dev, "logits")
     code = _dtype(logits, "logits")
     T, E = logits.shape
@@ -165,12 +167,11 @@ def route_grad(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, *,
     _same(idx, dev, "idx", (T, K), torch.int32)
     _same(dw, dev, "dw", (T, K), torch.float32)
     d = _route_desc(E, K, score, renorm, scale)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        ldo = _rows(out, dev, "out", E, T, logits.dtype)
-        check(lib.cco_route_grad(ctypes.byref(d), logits.data_ptr(), code, ld, idx.data_ptr(),
-                                 dw.data_ptr(), T, out.data_ptr(), ldo, on.ptr), "cco_route_grad")
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    ldo = _rows(out, dev, "out", E, T, logits.dtype)
+    check(lib.cco_route_grad(ctypes.byref(d), logits.data_ptr(), code, ld, idx.data_ptr(),
+                             dw.data_ptr(), T, out.data_ptr(), ldo, _current()), "cco_route_grad")
     return out
 
 
@@ -193,6 +194,9 @@ def group_product(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, w: 
     every group g.  x [rows, k] and w [groups, n, k] bf16 or fp16; rows of no
     group keep what `out` holds (undefined without `out`)."""
     dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return group_product(first, count, x, w, out=out)
     code = _dtype(x, "x", _HALF)
     ldx = _rows(x, dev, "x")
     rows, k = x.shape
@@ -201,12 +205,11 @@ def group_product(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, w: 
         raise ValueError("w must be [groups, n, k]")
     n = w.shape[1]
     _same(w, dev, "w", (g.groups, n, k), x.dtype)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((rows, n), dtype=x.dtype, device=dev)
-        ldy = _rows(out, dev, "out", n, rows, x.dtype)
-        check(lib.cco_group_product(ctypes.byref(g), code, x.data_ptr(), ldx, w.data_ptr(), n, k,
-                                    out.data_ptr(), ldy, on.ptr), "cco_group_product")
+    if out is None:
+        out = torch.empty((rows, n), dtype=x.dtype, device=dev)
+    ldy = _rows(out, dev, "out", n, rows, x.dtype)
+    check(lib.cco_group_product(ctypes.byref(g), code, x.data_ptr(), ldx, w.data_ptr(), n, k,
+                                out.data_ptr(), ldy, _current()), "cco_group_product")
     return out
 
 
@@ -215,6 +218,9 @@ def group_product_dx(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     """cco_group_product_dx: dx [rows, k], dx[r] = dy[r] w[g] for the rows r
     of every group g."""
     dev = _device(dy, "dy")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return group_product_dx(first, count, dy, w, out=out)
     code = _dtype(dy, "dy", _HALF)
     lddy = _rows(dy, dev, "dy")
     rows, n = dy.shape
@@ -223,13 +229,12 @@ def group_product_dx(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
         raise ValueError("w must be [groups, n, k]")
     k = w.shape[2]
     _same(w, dev, "w", (g.groups, n, k), dy.dtype)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((rows, k), dtype=dy.dtype, device=dev)
-        lddx = _rows(out, dev, "out", k, rows, dy.dtype)
-        check(lib.cco_group_product_dx(ctypes.byref(g), code, dy.data_ptr(), lddy, w.data_ptr(),
-                                       n, k, out.data_ptr(), lddx, on.ptr),
-              "cco_group_product_dx")
+    if out is None:
+        out = torch.empty((rows, k), dtype=dy.dtype, device=dev)
+    lddx = _rows(out, dev, "out", k, rows, dy.dtype)
+    check(lib.cco_group_product_dx(ctypes.byref(g), code, dy.data_ptr(), lddy, w.data_ptr(),
+                                   n, k, out.data_ptr(), lddx, _current()),
+          "cco_group_product_dx")
     return out
 
 
@@ -240,6 +245,9 @@ def group_product_dw(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     group g of dy[r]^T x[r], in the operands' type or, with an fp32 `out`, in
     fp32; with `accumulate` added to what `out` holds."""
     dev = _device(dy, "dy")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return group_product_dw(first, count, dy, x, out=out, accumulate=accumulate)
     code = _dtype(dy, "dy", _HALF)
     lddy = _rows(dy, dev, "dy")
     rows, n = dy.shape
@@ -248,13 +256,12 @@ def group_product_dw(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     g = _groups(first, count, rows, dev)
     if out is None and accumulate:
         raise ValueError("accumulate needs out")
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty((g.groups, n, k), dtype=dy.dtype, device=dev)
-        _same(out, dev, "out", (g.groups, n, k))
-        check(lib.cco_group_product_dw(ctypes.byref(g), code, dy.data_ptr(), lddy, x.data_ptr(),
-                                       ldx, n, k, out.data_ptr(), _dtype(out, "out"),
-                                       int(bool(accumulate)), on.ptr), "cco_group_product_dw")
+    if out is None:
+        out = torch.empty((g.groups, n, k), dtype=dy.dtype, device=dev)
+    _same(out, dev, "out", (g.groups, n, k))
+    check(lib.cco_group_product_dw(ctypes.byref(g), code, dy.data_ptr(), lddy, x.data_ptr(),
+                                   ldx, n, k, out.data_ptr(), _dtype(out, "out"),
+                                   int(bool(accumulate)), _current()), "cco_group_product_dw")
     return out
 
 
@@ -302,18 +309,21 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *,
     the norm of x.  x, y [T, hidden] bf16, fp16 or fp32, contiguous; post,
     pre and gate [hidden], fp32 or x's type; token_gate fp32 [T]."""
     dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return block_norm(x, y, post=post, gate=gate, token_gate=token_gate, pre=pre,
+                              scale=scale, eps=eps, out=out, u=u)
     _same(x, dev, "x")
     d = _norm_desc(x, post, gate, token_gate, pre, scale, eps)
     _same(y, dev, "y", x.shape, x.dtype)
-    with _On(dev, stream) as on:
-        if y is not None and out is None:
-            out = torch.empty_like(x)
-        if pre is not None and u is None:
-            u = torch.empty_like(x)
-        _same(out, dev, "out", x.shape, x.dtype)
-        _same(u, dev, "u", x.shape, x.dtype)
-        check(lib.cco_block_norm(ctypes.byref(d), x.data_ptr(), _p(y), x.shape[0], _p(out), _p(u),
-                                 on.ptr), "cco_block_norm")
+    if y is not None and out is None:
+        out = torch.empty_like(x)
+    if pre is not None and u is None:
+        u = torch.empty_like(x)
+    _same(out, dev, "out", x.shape, x.dtype)
+    _same(u, dev, "u", x.shape, x.dtype)
+    check(lib.cco_block_norm(ctypes.byref(d), x.data_ptr(), _p(y), x.shape[0], _p(out), _p(u),
+                             _current()), "cco_block_norm")
     return out, u
 
 
@@ -326,29 +336,32 @@ def block_norm_grad(x: torch.Tensor, y: torch.Tensor | None, dout: torch.Tensor 
     is nothing; dgate is the gradient of the gate that is given, and the
     gradients of post, gates and pre are fp32."""
     dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return block_norm_grad(x, y, dout, du, post=post, gate=gate, token_gate=token_gate,
+                                   pre=pre, scale=scale, eps=eps, dx=dx, dy=dy)
     _same(x, dev, "x")
     d = _norm_desc(x, post, gate, token_gate, pre, scale, eps)
     T, H = x.shape
     for name, t in (("y", y), ("dout", dout), ("du", du), ("dx", dx), ("dy", dy)):
         _same(t, dev, name, x.shape, x.dtype)
     f32 = torch.float32
-    with _On(dev, stream) as on:
-        if dx is None:
-            dx = torch.empty_like(x)
-        if y is not None and dy is None:
-            dy = torch.empty_like(x)
-        dpost = torch.empty(H, dtype=f32, device=dev) if post is not None else None
-        dpre = torch.empty(H, dtype=f32, device=dev) if pre is not None else None
-        dgate = None
-        if gate is not None:
-            dgate = torch.empty(H, dtype=f32, device=dev)
-        elif token_gate is not None:
-            dgate = torch.empty(T, dtype=f32, device=dev)
-        nbytes = lib.cco_block_norm_grad_workspace(ctypes.byref(d), T)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        check(lib.cco_block_norm_grad(ctypes.byref(d), x.data_ptr(), _p(y), _p(dout), _p(du), T,
-                                      dx.data_ptr(), _p(dy), _p(dpost), _p(dgate), _p(dpre),
-                                      _p(ws), nbytes, on.ptr), "cco_block_norm_grad")
+    if dx is None:
+        dx = torch.empty_like(x)
+    if y is not None and dy is None:
+        dy = torch.empty_like(x)
+    dpost = torch.empty(H, dtype=f32, device=dev) if post is not None else None
+    dpre = torch.empty(H, dtype=f32, device=dev) if pre is not None else None
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty(H, dtype=f32, device=dev)
+    elif token_gate is not None:
+        dgate = torch.empty(T, dtype=f32, device=dev)
+    nbytes = lib.cco_block_norm_grad_workspace(ctypes.byref(d), T)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    check(lib.cco_block_norm_grad(ctypes.byref(d), x.data_ptr(), _p(y), _p(dout), _p(du), T,
+                                  dx.data_ptr(), _p(dy), _p(dpost), _p(dgate), _p(dpre),
+                                  _p(ws), nbytes, _current()), "cco_block_norm_grad")
     return dx, dy, dpost, dgate, dpre
 
 
@@ -361,18 +374,23 @@ def combine_norm(moe: MoE, x: torch.Tensor, w: torch.Tensor, *, post: torch.Tens
     and block_norm of its result in one launch; y, the combined rows, only
     with keep_y (None otherwise).  x bf16 [T, hidden], w fp32 [T, K]."""
     dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return combine_norm(moe, x, w, post=post, gate=gate, token_gate=token_gate, pre=pre,
+                                scale=scale, eps=eps, out=out, u=u, keep_y=keep_y)
+    if dev.index != moe.heap.device:
+        raise ValueError("x must be on the layer's device")
     _same(x, dev, "x", None, torch.bfloat16)
     d = _norm_desc(x, post, gate, token_gate, pre, scale, eps)
     _same(w, dev, "w", (x.shape[0], moe.K), torch.float32)
-    with _On(dev, stream) as on:
-        if out is None:
-            out = torch.empty_like(x)
-        if pre is not None and u is None:
-            u = torch.empty_like(x)
-        _same(out, dev, "out", x.shape, x.dtype)
-        _same(u, dev, "u", x.shape, x.dtype)
-        y = torch.empty_like(x) if keep_y else None
-        check(lib.cco_moe_combine_norm(moe.handle, w.data_ptr(), ctypes.byref(d), x.data_ptr(),
-                                       x.shape[0], _p(y), _p(out), _p(u), on.ptr),
-              "cco_moe_combine_norm")
+    if out is None:
+        out = torch.empty_like(x)
+    if pre is not None and u is None:
+        u = torch.empty_like(x)
+    _same(out, dev, "out", x.shape, x.dtype)
+    _same(u, dev, "u", x.shape, x.dtype)
+    y = torch.empty_like(x) if keep_y else None
+    check(lib.cco_moe_combine_norm(moe.handle, w.data_ptr(), ctypes.byref(d), x.data_ptr(),
+                                   x.shape[0], _p(y), _p(out), _p(u), _current()),
+          "cco_moe_combine_norm")
     return out, u, y
