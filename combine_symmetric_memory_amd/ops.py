@@ -52,12 +52,14 @@ class _Elsewhere:
         return self._stack.__exit__(*exc)
 
 
+# torch's own query without the stream object around it (microseconds, which
+# a call for a few tokens would notice), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _away(dev: torch.device, stream) -> bool:
     return stream is not None or dev.index != torch.cuda.current_device()
-
-
-def _current() -> int:
-    return torch.cuda.current_stream().cuda_stream
 
 
 def _dtype(t: torch.Tensor, name: str, allowed=None) -> int:
@@ -92,20 +94,25 @@ def _rows(t: torch.Tensor, dev, name: str, cols: int | None = None, rows: int | 
     """A [rows][cols] tensor with contiguous rows; returns its row distance."""
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError("%s must be a tensor on %s" % (name, dev))
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or \
-       (rows is not None and t.shape[0] != rows):
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols) or \
+       (rows is not None and shape[0] != rows):
         raise ValueError("%s must be [%s, %s], got %s" % (
             name, "rows" if rows is None else rows, "columns" if cols is None else cols,
-            tuple(t.shape)))
+            tuple(shape)))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    r, c = shape
+    if t.is_contiguous():
+        return c or 1
+    ld, step = t.stride()
+    if c > 1 and step != 1:
         raise ValueError("the rows of %s must be contiguous" % name)
-    if t.shape[0] <= 1:
-        return max(1, t.shape[1])
-    if t.stride(0) < t.shape[1]:
+    if r <= 1:
+        return c or 1
+    if ld < c:
         raise ValueError("the rows of %s overlap" % name)
-    return max(1, t.stride(0))
+    return ld or 1
 
 
 def _p(t: torch.Tensor | None):
@@ -145,7 +152,7 @@ def route(logits: torch.Tensor, topk: int, *, score: str = "softmax", renorm: bo
     else:
         _same(w, dev, "w", (T, topk), torch.float32)
     check(lib.cco_route(ctypes.byref(d), logits.data_ptr(), code, ld, _p(bias), T,
-                        idx.data_ptr(), w.data_ptr(), _current()), "cco_route")
+                        idx.data_ptr(), w.data_ptr(), _raw_stream(dev.index)), "cco_route")
     return idx, w
 
 
@@ -168,10 +175,11 @@ def route_grad(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, *,
     _same(dw, dev, "dw", (T, K), torch.float32)
     d = _route_desc(E, K, score, renorm, scale)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    ldo = _rows(out, dev, "out", E, T, logits.dtype)
+        out, ldo = torch.empty((T, E), dtype=logits.dtype, device=dev), E
+    else:
+        ldo = _rows(out, dev, "out", E, T, logits.dtype)
     check(lib.cco_route_grad(ctypes.byref(d), logits.data_ptr(), code, ld, idx.data_ptr(),
-                             dw.data_ptr(), T, out.data_ptr(), ldo, _current()), "cco_route_grad")
+                             dw.data_ptr(), T, out.data_ptr(), ldo, _raw_stream(dev.index)), "cco_route_grad")
     return out
 
 
@@ -209,7 +217,7 @@ def group_product(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, w: 
         out = torch.empty((rows, n), dtype=x.dtype, device=dev)
     ldy = _rows(out, dev, "out", n, rows, x.dtype)
     check(lib.cco_group_product(ctypes.byref(g), code, x.data_ptr(), ldx, w.data_ptr(), n, k,
-                                out.data_ptr(), ldy, _current()), "cco_group_product")
+                                out.data_ptr(), ldy, _raw_stream(dev.index)), "cco_group_product")
     return out
 
 
@@ -233,7 +241,7 @@ def group_product_dx(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
         out = torch.empty((rows, k), dtype=dy.dtype, device=dev)
     lddx = _rows(out, dev, "out", k, rows, dy.dtype)
     check(lib.cco_group_product_dx(ctypes.byref(g), code, dy.data_ptr(), lddy, w.data_ptr(),
-                                   n, k, out.data_ptr(), lddx, _current()),
+                                   n, k, out.data_ptr(), lddx, _raw_stream(dev.index)),
           "cco_group_product_dx")
     return out
 
@@ -261,42 +269,37 @@ def group_product_dw(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     _same(out, dev, "out", (g.groups, n, k))
     check(lib.cco_group_product_dw(ctypes.byref(g), code, dy.data_ptr(), lddy, x.data_ptr(),
                                    ldx, n, k, out.data_ptr(), _dtype(out, "out"),
-                                   int(bool(accumulate)), _current()), "cco_group_product_dw")
+                                   int(bool(accumulate)), _raw_stream(dev.index)), "cco_group_product_dw")
     return out
 
 
 # ---------------------------------------------------- norms around a block --
 def _norm_desc(x: torch.Tensor, post, gate, token_gate, pre, scale, eps):
-    dev = x.device
+    dev, dtype = x.device, x.dtype
     if x.dim() != 2:
         raise ValueError("x must be [T, hidden]")
     T, H = x.shape
-    kind = _capi.CCO_GATE_NONE
+    code = _dtype(x, "x")
     wdtype = None
-    vectors = [("post", post), ("pre", pre)]
+    for name, v in (("post", post), ("pre", pre), ("gate", gate)):
+        if v is not None:
+            _same(v, dev, name, (H,))
+            if wdtype is None:
+                wdtype = v.dtype
+                if wdtype != torch.float32 and wdtype != dtype:
+                    raise ValueError("post, pre and gate must be fp32 or of x's type")
+            elif v.dtype != wdtype:
+                raise ValueError("post, pre and gate must share one type")
+    kind = _capi.CCO_GATE_NONE
     if gate is not None:
         if token_gate is not None:
             raise ValueError("gate and token_gate exclude each other")
         kind = _capi.CCO_GATE_CHANNEL
-        vectors.append(("gate", gate))
     elif token_gate is not None:
         _same(token_gate, dev, "token_gate", (T,), torch.float32)
-        kind = _capi.CCO_GATE_TOKEN
-    for name, v in vectors:
-        if v is None:
-            continue
-        _same(v, dev, name, (H,))
-        if wdtype is not None and v.dtype != wdtype:
-            raise ValueError("post, pre and a channel gate must share one type")
-        wdtype = v.dtype
-    if wdtype is None:
-        wdtype = x.dtype
-    code = _dtype(x, "x")
-    if wdtype not in (torch.float32, x.dtype):
-        raise ValueError("post, pre and gate must be fp32 or of x's type")
-    return _capi.cco_block_norm_desc(H, code, _DTYPES[wdtype], kind, float(scale), float(eps),
-                                     _p(post), _p(gate if token_gate is None else token_gate),
-                                     _p(pre))
+        kind, gate = _capi.CCO_GATE_TOKEN, token_gate
+    return _capi.cco_block_norm_desc(H, code, code if wdtype is None else _DTYPES[wdtype], kind,
+                                     scale, eps, _p(post), _p(gate), _p(pre))
 
 
 def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *,
@@ -316,14 +319,16 @@ def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, *,
     _same(x, dev, "x")
     d = _norm_desc(x, post, gate, token_gate, pre, scale, eps)
     _same(y, dev, "y", x.shape, x.dtype)
-    if y is not None and out is None:
+    if out is not None:
+        _same(out, dev, "out", x.shape, x.dtype)
+    elif y is not None:
         out = torch.empty_like(x)
-    if pre is not None and u is None:
+    if u is not None:
+        _same(u, dev, "u", x.shape, x.dtype)
+    elif pre is not None:
         u = torch.empty_like(x)
-    _same(out, dev, "out", x.shape, x.dtype)
-    _same(u, dev, "u", x.shape, x.dtype)
     check(lib.cco_block_norm(ctypes.byref(d), x.data_ptr(), _p(y), x.shape[0], _p(out), _p(u),
-                             _current()), "cco_block_norm")
+                             _raw_stream(dev.index)), "cco_block_norm")
     return out, u
 
 
@@ -361,7 +366,7 @@ def block_norm_grad(x: torch.Tensor, y: torch.Tensor | None, dout: torch.Tensor 
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     check(lib.cco_block_norm_grad(ctypes.byref(d), x.data_ptr(), _p(y), _p(dout), _p(du), T,
                                   dx.data_ptr(), _p(dy), _p(dpost), _p(dgate), _p(dpre),
-                                  _p(ws), nbytes, _current()), "cco_block_norm_grad")
+                                  _p(ws), nbytes, _raw_stream(dev.index)), "cco_block_norm_grad")
     return dx, dy, dpost, dgate, dpre
 
 
@@ -391,6 +396,6 @@ def combine_norm(moe: MoE, x: torch.Tensor, w: torch.Tensor, *, post: torch.Tens
     _same(u, dev, "u", x.shape, x.dtype)
     y = torch.empty_like(x) if keep_y else None
     check(lib.cco_moe_combine_norm(moe.handle, w.data_ptr(), ctypes.byref(d), x.data_ptr(),
-                                   x.shape[0], _p(y), _p(out), _p(u), _current()),
+                                   x.shape[0], _p(y), _p(out), _p(u), _raw_stream(dev.index)),
           "cco_moe_combine_norm")
     return out, u, y
