@@ -39,27 +39,59 @@ struct Raw8 {
   T v[8];
 };
 
-// Elements [at, at + 8) of a row of H, zeros past its end.
+// The elements n, n + 1, ... of r, zeros behind (n uniform over the row's
+// last vector; 0..7).
 template <class T>
-__device__ __forceinline__ Raw8<T> load8(const T *row, int at, int H) {
-  Raw8<T> r;
-  if (at + 8 <= H) {
-    __builtin_memcpy(&r, row + at, sizeof(r));
-  } else {
+__device__ __forceinline__ Raw8<T> drop_first(Raw8<T> r, int n) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) r.v[c] = at + c < H ? row[at + c] : (T)0.0f;
-  }
+  for (int step = 4; step > 0; step /= 2)
+    if (n & step) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) r.v[c] = c + step < 8 ? r.v[c + step] : (T)0.0f;
+    }
   return r;
 }
 
-template <class T>
+// How a row of H ends: in whole vectors of eight, inside one, or before the
+// first one is full.  A property of the kernel, so that no branch stands
+// around a load (the compiler would wait for the load where it ends).
+enum RowEnd { kWhole, kInside, kShort };
+inline RowEnd row_end(int H) { return H % 8 == 0 ? kWhole : (H > 8 ? kInside : kShort); }
+
+// Elements [at, at + 8) of a row of H.  Past H - 8 the row's last eight are
+// loaded instead; cut8, which waits for the load, moves those down that
+// belong to the vector and puts zeros behind the row's end.
+template <RowEnd END, class T>
+__device__ __forceinline__ Raw8<T> load8(const T *row, int at, int H) {
+  Raw8<T> r;
+  if constexpr (END == kShort) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) r.v[c] = row[min(at + c, H - 1)];
+  } else {
+    __builtin_memcpy(&r, row + min(at, H - 8), sizeof(r));
+  }
+  return r;
+}
+template <RowEnd END, class T>
+__device__ __forceinline__ Raw8<T> cut8(Raw8<T> r, int at, int H) {
+  if constexpr (END == kInside) {
+    const Raw8<T> tail = drop_first(r, 8 - H % 8);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) r.v[c] = at + 8 > H ? tail.v[c] : r.v[c];
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) r.v[c] = (END == kShort ? at + c : at) < H ? r.v[c] : (T)0.0f;
+  return r;
+}
+
+template <RowEnd END, class T>
 __device__ __forceinline__ void store8(T *row, int at, int H, const float *v) {
   Raw8<T> r;
 #pragma unroll
   for (int c = 0; c < 8; ++c) r.v[c] = (T)v[c];
-  if (at + 8 <= H) {
+  if (END == kWhole ? at < H : at + 8 <= H) {
     __builtin_memcpy(row + at, &r, sizeof(r));
-  } else {
+  } else if (END != kWhole) {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (at + c < H) row[at + c] = r.v[c];
@@ -67,28 +99,32 @@ __device__ __forceinline__ void store8(T *row, int at, int H, const float *v) {
 }
 
 // A thread's share of a row: NV vectors, vector i at (i * threads + t) * 8.
-template <class T, int NV>
+template <RowEnd END, class T, int NV>
 struct RowRaw {
   Raw8<T> v[NV];
   __device__ __forceinline__ void load(const T *row, int H) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = load8(row, (i * blockDim.x + threadIdx.x) * 8, H);
+    for (int i = 0; i < NV; ++i) v[i] = load8<END>(row, (i * blockDim.x + threadIdx.x) * 8, H);
   }
-  __device__ __forceinline__ void get(float (&f)[NV * 8]) const {
+  __device__ __forceinline__ void get(int H, float (&f)[NV * 8]) const {
 #pragma unroll
-    for (int i = 0; i < NV * 8; ++i) f[i] = (float)v[i / 8].v[i % 8];
+    for (int i = 0; i < NV; ++i) {
+      const Raw8<T> r = cut8<END>(v[i], (i * blockDim.x + threadIdx.x) * 8, H);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[i * 8 + c] = (float)r.v[c];
+    }
   }
 };
 
-template <class T, int NV>
+template <RowEnd END, class T, int NV>
 __device__ __forceinline__ void store_row(T *row, int H, const float (&v)[NV * 8]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    store8(row, (i * blockDim.x + threadIdx.x) * 8, H, v + i * 8);
+    store8<END>(row, (i * blockDim.x + threadIdx.x) * 8, H, v + i * 8);
 }
 
 // A parameter vector's elements of this thread (1 where absent).
-template <class T, int NV>
+template <RowEnd END, class T, int NV>
 __device__ __forceinline__ void load_param(const void *p, int f32, int H, float (&v)[NV * 8]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -97,11 +133,11 @@ __device__ __forceinline__ void load_param(const void *p, int f32, int H, float 
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[i * 8 + c] = 1.0f;
     } else if (f32) {
-      const Raw8<float> r = load8((const float *)p, at, H);
+      const Raw8<float> r = cut8<END>(load8<END>((const float *)p, at, H), at, H);
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[i * 8 + c] = r.v[c];
     } else {
-      const Raw8<T> r = load8((const T *)p, at, H);
+      const Raw8<T> r = cut8<END>(load8<END>((const T *)p, at, H), at, H);
 #pragma unroll
       for (int c = 0; c < 8; ++c) v[i * 8 + c] = (float)r.v[c];
     }
@@ -109,11 +145,11 @@ __device__ __forceinline__ void load_param(const void *p, int f32, int H, float 
 }
 
 // gate * post of this thread's elements.
-template <class T, int NV>
+template <RowEnd END, class T, int NV>
 __device__ __forceinline__ void load_gate_post(const NormArgs &a, float (&v)[NV * 8]) {
   float g[NV * 8];
-  load_param<T, NV>(a.post, a.w_f32, a.H, v);
-  load_param<T, NV>(a.gate_kind == CCO_GATE_CHANNEL ? a.gate : nullptr, a.w_f32, a.H, g);
+  load_param<END, T, NV>(a.post, a.w_f32, a.H, v);
+  load_param<END, T, NV>(a.gate_kind == CCO_GATE_CHANNEL ? a.gate : nullptr, a.w_f32, a.H, g);
 #pragma unroll
   for (int i = 0; i < NV * 8; ++i) v[i] *= g[i];
 }
@@ -165,6 +201,12 @@ __device__ __forceinline__ float rms_inverse(float sum, int H, float eps) {
   return 1.0f / sqrtf(sum / (float)H + eps);
 }
 
+// The row this workgroup takes after row t, or t again behind the last (its
+// elements are then loaded and not used: no branch around the loads).
+__device__ __forceinline__ int next_row(int t, int T) {
+  return t < T - (int)gridDim.x ? t + (int)gridDim.x : t;
+}
+
 __device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // A thread's share of combine's output row of token t, rounded to bf16: the
@@ -172,7 +214,7 @@ __device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_read
 // multiple of 8 and the windows are aligned.)
 template <int NV>
 __device__ __forceinline__ void combine_row(const CombineView &c, int t, int H,
-                                            RowRaw<__bf16, NV> &out) {
+                                            RowRaw<kWhole, __bf16, NV> &out) {
   const MoeArgs &a = c.moe;
   float y[NV * 8];
 #pragma unroll
@@ -219,24 +261,29 @@ __device__ __forceinline__ void combine_row(const CombineView &c, int t, int H,
   for (int i = 0; i < NV * 8; ++i) out.v[i / 8].v[i % 8] = (__bf16)y[i];
 }
 
-template <class T, int NV, bool COMBINE>
+template <RowEnd END, class T, int NV, bool COMBINE>
 __device__ __forceinline__ void norm_rows(const NormArgs &a, const CombineView *cv) {
   constexpr int N = NV * 8;
   __shared__ float lds[2 * kMaxWaves * kMaxSums];
   int half = 0;
   const int waves = blockDim.x / kWave, H = a.H;
   const bool has_y = COMBINE || a.y;
-  RowRaw<T, NV> rx, ry;
+  // an absent y is read as x and not used: no branch around the loads
+  const T *yrow = (const T *)(a.y ? a.y : a.x);
+  RowRaw<END, T, NV> rx, ry;
+  const bool token = a.gate_kind == CCO_GATE_TOKEN;
+  float tgate = 1.0f;  // the token's gate; first of the loads, which return in order
   auto fetch = [&](int t) __attribute__((always_inline)) {
+    if (token) tgate = ((const float *)a.gate)[t];
     rx.load((const T *)a.x + (int64_t)t * H, H);
-    if constexpr (!COMBINE)
-      if (has_y) ry.load((const T *)a.y + (int64_t)t * H, H);
+    if constexpr (!COMBINE) ry.load(yrow + (int64_t)t * H, H);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the row's work
   };
   int t = blockIdx.x;
   fetch(t);
   float gp[N], pre[N];
-  load_gate_post<T, NV>(a, gp);
-  load_param<T, NV>(a.pre, a.w_f32, H, pre);
+  load_gate_post<END, T, NV>(a, gp);
+  load_param<END, T, NV>(a.pre, a.w_f32, H, pre);
   for (; t < a.T; t += gridDim.x) {
     const int64_t off = (int64_t)t * H;
     float o[N], y[N];
@@ -250,12 +297,11 @@ __device__ __forceinline__ void norm_rows(const NormArgs &a, const CombineView *
         }
       }
     }
-    rx.get(o);
-    if (has_y) ry.get(y);
-    if (t + (int)gridDim.x < a.T) fetch(t + gridDim.x);
+    rx.get(H, o);
+    if (has_y) ry.get(H, y);
+    float s = a.scale * tgate;
+    fetch(next_row(t, a.T));
     if (has_y) {
-      float s = a.scale;
-      if (a.gate_kind == CCO_GATE_TOKEN) s *= ((const float *)a.gate)[t];
       if (a.post) {
         float sum[1] = {0.0f};
 #pragma unroll
@@ -265,7 +311,7 @@ __device__ __forceinline__ void norm_rows(const NormArgs &a, const CombineView *
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(s * gp[i], y[i], o[i]);
-      if (a.out) store_row<T, NV>((T *)a.out + off, H, o);
+      if (a.out) store_row<END, T, NV>((T *)a.out + off, H, o);
     }
     if (a.u) {
       float sum[1] = {0.0f};
@@ -275,25 +321,25 @@ __device__ __forceinline__ void norm_rows(const NormArgs &a, const CombineView *
       const float r = rms_inverse(sum[0], H, a.eps);
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i] = o[i] * r * pre[i];
-      store_row<T, NV>((T *)a.u + off, H, o);
+      store_row<END, T, NV>((T *)a.u + off, H, o);
     }
   }
 }
 
-template <class T, int NV, int MAXT>
+template <RowEnd END, class T, int NV, int MAXT>
 __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs a) {
-  norm_rows<T, NV, false>(a, nullptr);
+  norm_rows<END, T, NV, false>(a, nullptr);
 }
 
 template <int NV, int MAXT>
 __global__ __launch_bounds__(MAXT) void combine_norm_kernel(CombineView c, NormArgs a) {
-  norm_rows<__bf16, NV, true>(a, &c);
+  norm_rows<kWhole, __bf16, NV, true>(a, &c);
 }
 
 // KEEP: the vectors stay in registers and the next row is fetched ahead;
 // otherwise (rows of more than 512 threads, whose register budget is half)
 // both are read when they are needed.
-template <class T, int NV, int MAXT, bool KEEP>
+template <RowEnd END, class T, int NV, int MAXT, bool KEEP>
 __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
   constexpr int N = NV * 8;
   __shared__ float lds[2 * kMaxWaves * kMaxSums];
@@ -301,23 +347,27 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
   const int waves = blockDim.x / kWave, H = a.H;
   const float inv_h = 1.0f / (float)H;
   const bool token = a.gate_kind == CCO_GATE_TOKEN;
-  RowRaw<T, NV> rx, ry, rd, rq;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    ry.v[i / 8].v[i % 8] = rd.v[i / 8].v[i % 8] = rq.v[i / 8].v[i % 8] = (T)0.0f;
+  // an absent y, dout or du is read as x and then taken as zeros: no branch
+  // around the loads
+  const T *yrow = (const T *)(a.y ? a.y : a.x), *drow = (const T *)(a.dout ? a.dout : a.x),
+          *qrow = (const T *)(a.du ? a.du : a.x);
+  RowRaw<END, T, NV> rx, ry, rd, rq;
+  float tgate = 1.0f;  // the token's gate; first of the loads, which return in order
   auto fetch = [&](int t) __attribute__((always_inline)) {
     const int64_t off = (int64_t)t * H;
-    if (a.y) ry.load((const T *)a.y + off, H);
+    if (token) tgate = ((const float *)a.gate)[t];
+    ry.load(yrow + off, H);
     rx.load((const T *)a.x + off, H);
-    if (a.dout) rd.load((const T *)a.dout + off, H);
-    if (a.du) rq.load((const T *)a.du + off, H);
+    rd.load(drow + off, H);
+    rq.load(qrow + off, H);
+    __builtin_amdgcn_sched_barrier(0);  // the loads stay ahead of the row's work
   };
   int t = blockIdx.x;
   if (KEEP) fetch(t);
   float gp[N], pre[N], csum[N], dpre[N];
   if (KEEP) {
-    load_gate_post<T, NV>(a, gp);
-    load_param<T, NV>(a.pre, a.w_f32, H, pre);
+    load_gate_post<END, T, NV>(a, gp);
+    load_param<END, T, NV>(a.pre, a.w_f32, H, pre);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) csum[i] = dpre[i] = 0.0f;
@@ -326,15 +376,22 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
     float x[N], y[N], d[N], q[N];
     if (!KEEP) {
       fetch(t);
-      load_gate_post<T, NV>(a, gp);
-      load_param<T, NV>(a.pre, a.w_f32, H, pre);
+      load_gate_post<END, T, NV>(a, gp);
+      load_param<END, T, NV>(a.pre, a.w_f32, H, pre);
     }
-    rx.get(x);
-    ry.get(y);
-    rd.get(d);
-    rq.get(q);
-    if (KEEP && t + (int)gridDim.x < a.T) fetch(t + gridDim.x);
-    const float tg = token ? ((const float *)a.gate)[t] : 1.0f;
+    rx.get(H, x);
+    ry.get(H, y);
+    rd.get(H, d);
+    rq.get(H, q);
+    auto absent = [&](float (&v)[N]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    };
+    if (!a.y) absent(y);
+    if (!a.dout) absent(d);
+    if (!a.du) absent(q);
+    const float tg = tgate;
+    if (KEEP) fetch(next_row(t, a.T));
     float ry1 = 1.0f;
     if (a.post) {
       float s[1] = {0.0f};
@@ -371,16 +428,16 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
       csum[i] = __builtin_fmaf(sd, y[i], csum[i]);
       q[i] = __builtin_fmaf(-y[i], by, sd * gp[i]);
     }
-    store_row<T, NV>((T *)a.dx + off, H, d);
-    if (a.dy) store_row<T, NV>((T *)a.dy + off, H, q);
+    store_row<END, T, NV>((T *)a.dx + off, H, d);
+    if (a.dy) store_row<END, T, NV>((T *)a.dy + off, H, q);
   }
   // this workgroup's column sums: [sum][workgroup][H]
   float *part = a.partial + (int64_t)blockIdx.x * H;
   if (a.dpost || a.gate_kind == CCO_GATE_CHANNEL) {
-    store_row<float, NV>(part, H, csum);
+    store_row<END, float, NV>(part, H, csum);
     part += (int64_t)gridDim.x * H;
   }
-  if (a.dpre) store_row<float, NV>(part, H, dpre);
+  if (a.dpre) store_row<END, float, NV>(part, H, dpre);
 }
 
 // Columns of the partial sums, added in fixed order: 16 chains of every 16th
@@ -427,33 +484,56 @@ int row_grid(int64_t T, int threads, int per_cu) {
   return (int)std::min<int64_t>(T, (int64_t)kNumCus * std::max(1, per_cu / threads));
 }
 
-template <class T>
-hipError_t launch_norm(const NormArgs &a, hipStream_t st) {
-  if (a.T == 0) return hipSuccess;
+template <RowEnd END, class T>
+hipError_t launch_norm_as(const NormArgs &a, hipStream_t st) {
   const RowShape rs = row_shape(a.H);
   const dim3 grid(row_grid(a.T, rs.threads, 1024)), block(rs.threads);
   if (rs.nv == 1)
-    hipLaunchKernelGGL((norm_kernel<T, 1, 512>), grid, block, 0, st, a);
-  else if (rs.threads <= 512)
-    hipLaunchKernelGGL((norm_kernel<T, 2, 512>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_kernel<T, 2, 1024>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_kernel<END, T, 1, 512>), grid, block, 0, st, a);
+  else if constexpr (END != kShort) {
+    if (rs.threads <= 512)
+      hipLaunchKernelGGL((norm_kernel<END, T, 2, 512>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((norm_kernel<END, T, 2, 1024>), grid, block, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_norm(const NormArgs &a, hipStream_t st) {
+  if (a.T == 0) return hipSuccess;
+  switch (row_end(a.H)) {
+    case kWhole: return launch_norm_as<kWhole, T>(a, st);
+    case kInside: return launch_norm_as<kInside, T>(a, st);
+    default: return launch_norm_as<kShort, T>(a, st);
+  }
+}
+
+template <RowEnd END, class T>
+hipError_t launch_grad_as(const NormArgs &a, int nwg, hipStream_t st) {
+  const RowShape rs = row_shape(a.H);
+  const dim3 grid(nwg), block(rs.threads);
+  if (rs.nv == 1)
+    hipLaunchKernelGGL((norm_grad_kernel<END, T, 1, 512, true>), grid, block, 0, st, a);
+  else if constexpr (END != kShort) {
+    if (rs.threads <= 512)
+      hipLaunchKernelGGL((norm_grad_kernel<END, T, 2, 512, true>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((norm_grad_kernel<END, T, 2, 1024, false>), grid, block, 0, st, a);
+  }
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_grad(const NormArgs &a, hipStream_t st) {
-  const RowShape rs = row_shape(a.H);
   const int nwg = norm_grad_workgroups(a.H, a.T);
   if (nwg > 0) {
-    const dim3 grid(nwg), block(rs.threads);
-    if (rs.nv == 1)
-      hipLaunchKernelGGL((norm_grad_kernel<T, 1, 512, true>), grid, block, 0, st, a);
-    else if (rs.threads <= 512)
-      hipLaunchKernelGGL((norm_grad_kernel<T, 2, 512, true>), grid, block, 0, st, a);
-    else
-      hipLaunchKernelGGL((norm_grad_kernel<T, 2, 1024, false>), grid, block, 0, st, a);
-    const hipError_t err = hipGetLastError();
+    hipError_t err;
+    switch (row_end(a.H)) {
+      case kWhole: err = launch_grad_as<kWhole, T>(a, nwg, st); break;
+      case kInside: err = launch_grad_as<kInside, T>(a, nwg, st); break;
+      default: err = launch_grad_as<kShort, T>(a, nwg, st);
+    }
     if (err != hipSuccess) return err;
   }
   const int sums = (a.dpost || a.gate_kind == CCO_GATE_CHANNEL) + (a.dpre != nullptr);
