@@ -25,6 +25,7 @@
 // kernel (no atomics).
 #include "combine_impl.h"
 #include "ops_internal.h"
+#include "wave_ops.h"
 
 namespace cco {
 namespace {
@@ -152,24 +153,6 @@ __device__ __forceinline__ void load_gate_post(const NormArgs &a, float (&v)[NV 
   load_param<END, T, NV>(a.gate_kind == CCO_GATE_CHANNEL ? a.gate : nullptr, a.w_f32, a.H, g);
 #pragma unroll
   for (int i = 0; i < NV * 8; ++i) v[i] *= g[i];
-}
-
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL,
-                                                               0xF, 0xF, true));
-}
-__device__ __forceinline__ float lane_value(float v, int l) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
-}
-// Sum over the wavefront, the same in every lane: pairs, quads, halves of 16
-// and 16 lanes by data-parallel moves, then the four rows of 16 in order.
-__device__ __forceinline__ float wave_total(float v) {
-  v += dpp<0xB1>(v);   // quad_perm 1 0 3 2
-  v += dpp<0x4E>(v);   // quad_perm 2 3 0 1
-  v += dpp<0x141>(v);  // mirror within 8
-  v += dpp<0x140>(v);  // mirror within 16
-  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
 // Sums of N values over the workgroup (every thread gets them, in one order

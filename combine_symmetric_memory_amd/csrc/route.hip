@@ -2,14 +2,15 @@
 // weights' gradient (include/cco_ops.h).
 //
 // One wavefront per token; lane l holds logits l, l + 64, ...  The K largest
-// choice values are taken one after the other: each lane keeps its best
+// choice values are taken one after the other: each lane offers its best
 // remaining candidate, the wavefront's largest is found by a reduction over
-// the lanes and removed.  Choice values are compared as integers that order
+// the lanes (data-parallel moves, no LDS) and removed.  Choice values are compared as integers that order
 // like the floating-point numbers (sign bit flipped, negative numbers
 // inverted), with the lower id first among equals.  Sums of scores with a
 // bias are formed in 64 bits, so that values next to a border do not change
 // places by rounding.
 #include "ops_internal.h"
+#include "wave_ops.h"
 
 namespace cco {
 namespace {
@@ -32,22 +33,6 @@ __device__ __forceinline__ void store_logit(void *p, int64_t i, float v) {
     ((float *)p)[i] = v;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
-  return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
-  return v;
-}
-
 // Integers that order like the numbers; NaN like -inf, and -0 like +0; 0 is
 // below all.
 __device__ __forceinline__ uint64_t order_key(double v) {
@@ -57,22 +42,38 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return (b >> 63) ? ~b : (b | (1ull << 63));
 }
 
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v == v)) v = -__builtin_inff();
+  v += 0.0f;
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  return (b >> 31) ? ~b : (b | (1u << 31));
+}
+
+__device__ __forceinline__ int uniform_wave() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+}
+
 // exp(l - m) with m the largest: 0 for masked logits even if all are.
 __device__ __forceinline__ float exp_below(float l, float m) {
   return l == -__builtin_inff() ? 0.0f : expf(l - m);
 }
 
-// The largest (key, lowest id) over the wavefront.
-__device__ __forceinline__ void wave_best(uint64_t &key, int &id) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const uint64_t k2 = __shfl_xor((unsigned long long)key, d, kWave);
-    const int i2 = __shfl_xor(id, d, kWave);
-    if (k2 > key || (k2 == key && i2 < id)) {
-      key = k2;
-      id = i2;
-    }
+// The lane-wise best candidates' best: the largest (hi, lo), the lowest id
+// among equals.  Most rounds end after the first reduction.
+template <bool WIDE>
+__device__ __forceinline__ int wave_best(uint32_t hi, uint32_t lo, int id) {
+  const uint32_t top = wave_largest(hi);
+  uint64_t tied = __ballot(hi == top);
+  if (WIDE && (tied & (tied - 1))) {
+    const uint32_t low = hi == top ? lo : 0u;
+    const uint32_t best = wave_largest(low);
+    tied = __ballot(hi == top && lo == best);
   }
+  if (tied & (tied - 1)) {
+    const bool in = (tied >> (threadIdx.x % kWave)) & 1;
+    return (int)wave_smallest(in ? (uint32_t)id : 0xFFFFFFFFu);
+  }
+  return (int)lane_value((uint32_t)id, __builtin_ctzll(tied));
 }
 
 // Which experts' groups stay: bit g of the result.  c: choice values of the
@@ -104,7 +105,7 @@ __device__ __forceinline__ uint64_t kept_groups(const double *c, int E, int grou
   const uint64_t key = order_key(score);
   int rank = 0;
   for (int h = 0; h < groups; ++h) {
-    const uint64_t other = __shfl((unsigned long long)key, h * lanes, kWave);
+    const uint64_t other = lane_value(key, h * lanes);
     rank += other > key || (other == key && h < g);
   }
   // lane g * lanes speaks for group g
@@ -114,14 +115,16 @@ __device__ __forceinline__ uint64_t kept_groups(const double *c, int E, int grou
   return mask;
 }
 
-template <int DT, int EPL>
+// SCORED: the choice goes by scores (a bias or groups), in 64 bits; otherwise
+// by the logits' own order, 32 bits.
+template <int DT, int EPL, bool SCORED>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteArgs a) {
   extern __shared__ double choice[];  // [waves][E], with groups only
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int t = blockIdx.x * kRouteWaves + wave;
+  const int wave = uniform_wave(), lane = threadIdx.x % kWave;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / kWave) + wave;
   if (t >= a.T) return;
   const int E = a.E;
-  const int64_t row = (int64_t)t * a.ld;
+  const int64_t row = t * a.ld;
   const float low = -__builtin_inff();
   float l[EPL];
   float m = low;
@@ -131,10 +134,10 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteArgs a) 
     l[i] = e < E ? load_logit<DT>(a.logits, row + e) : low;
     m = fmaxf(m, l[i]);
   }
-  m = wave_max(m);
-  uint64_t key[EPL];
-  const bool scored = a.bias || a.groups > 1;
-  if (scored) {
+  m = wave_largest(m);
+  uint32_t hi[EPL], lo[SCORED ? EPL : 1];
+  if constexpr (SCORED) {
+    uint64_t key[EPL];
     double c[EPL];
     double sum = 0.0;
 #pragma unroll
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteArgs a) 
         c[i] = 1.0 / (1.0 + exp(-d));
       }
     }
-    if (a.score == CCO_SCORE_SOFTMAX) sum = wave_sum(sum);
+    if (a.score == CCO_SCORE_SOFTMAX) sum = wave_total(sum);
     double *cw = choice + wave * E;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -171,34 +174,42 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteArgs a) 
         if (e < E && !((mask >> (e / per)) & 1)) key[i] = 0;
       }
     }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      hi[i] = (uint32_t)(key[i] >> 32);
+      lo[i] = (uint32_t)key[i];
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      key[i] = lane + i * kWave < E ? order_key((double)l[i]) : 0;
+    for (int i = 0; i < EPL; ++i) hi[i] = lane + i * kWave < E ? order_key(l[i]) : 0;
   }
   // K rounds; lane j keeps the id of round j
   int mine = 0;
   for (int j = 0; j < a.K; ++j) {
-    uint64_t best = 0;
-    int id = 1 << 30;
+    uint32_t bh = hi[0], bl = SCORED ? lo[0] : 0;
+    int id = lane;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
+    for (int i = 1; i < EPL; ++i)
+      if (hi[i] > bh || (SCORED && hi[i] == bh && lo[SCORED ? i : 0] > bl)) {
+        bh = hi[i];
+        if (SCORED) bl = lo[SCORED ? i : 0];
         id = lane + i * kWave;
       }
-    wave_best(best, id);
+    id = wave_best<SCORED>(bh, bl, id);
     if (lane == j) mine = id;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (lane + i * kWave == id) key[i] = 0;
+      if (lane + i * kWave == id) {
+        hi[i] = 0;
+        if (SCORED) lo[SCORED ? i : 0] = 0;
+      }
   }
   // weights, lane j for round j
   const bool on = lane < a.K;
   const float lc = on ? load_logit<DT>(a.logits, row + mine) : low;
   float w;
   if (a.renorm) {
-    const float mc = wave_max(lc);
+    const float mc = wave_largest(lc);
     float s;
     if (a.score == CCO_SCORE_SOFTMAX) {
       s = exp_below(lc, mc);
@@ -209,20 +220,20 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteArgs a) 
       s = lc > 0.0f ? expf(-down) / (1.0f + expf(-lc)) : exp_below(lc, down) / (1.0f + expf(lc));
     }
     if (!on) s = 0.0f;
-    const float total = wave_sum(s);
+    const float total = wave_total(s);
     w = total == 0.0f ? 0.0f : s / total;
   } else if (a.score == CCO_SCORE_SOFTMAX) {
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sum += exp_below(l[i], m);
-    sum = wave_sum(sum);
+    sum = wave_total(sum);
     w = sum == 0.0f ? 0.0f : exp_below(lc, m) / sum;
   } else {
     w = lc > 0.0f ? 1.0f / (1.0f + expf(-lc)) : expf(lc) / (1.0f + expf(lc));
   }
   if (on) {
-    a.idx[(int64_t)t * a.K + lane] = mine;
-    a.w[(int64_t)t * a.K + lane] = w * a.scale;
+    a.idx[t * a.K + lane] = mine;
+    a.w[t * a.K + lane] = w * a.scale;
   }
 }
 
@@ -236,18 +247,18 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteArgs a) 
 //             normalisation cancels)
 template <int DT, int EPL>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_grad_kernel(RouteArgs a) {
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-  const int t = blockIdx.x * kRouteWaves + wave;
+  const int wave = uniform_wave(), lane = threadIdx.x % kWave;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / kWave) + wave;
   if (t >= a.T) return;
   const int E = a.E;
-  const int64_t row = (int64_t)t * a.ld, drow = (int64_t)t * a.lddl;
+  const int64_t row = t * a.ld, drow = t * a.lddl;
   const float low = -__builtin_inff();
   int id = -1;
   float dw = 0.0f, lc = low;
   if (lane < a.K) {
-    id = a.idx[(int64_t)t * a.K + lane];
+    id = a.idx[t * a.K + lane];
     if ((unsigned)id < (unsigned)E) {
-      dw = a.dw[(int64_t)t * a.K + lane];
+      dw = a.dw[t * a.K + lane];
       lc = load_logit<DT>(a.logits, row + id);
     } else {
       id = -1;
@@ -264,21 +275,21 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_grad_kernel(RouteArg
       p[i] = e < E ? load_logit<DT>(a.logits, row + e) : low;
       m = fmaxf(m, p[i]);
     }
-    m = wave_max(m);
+    m = wave_largest(m);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       p[i] = exp_below(p[i], m);
       sum += p[i];
     }
-    sum = wave_sum(sum);
+    sum = wave_total(sum);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) p[i] *= inv;
     part = on ? a.scale * dw * (exp_below(lc, m) * inv) : 0.0f;
-    down_all = wave_sum(part);
+    down_all = wave_total(part);
   } else if (a.renorm) {
-    const float mc = wave_max(lc);
+    const float mc = wave_largest(lc);
     float s, other = 1.0f;  // other: 1 - score (sigmoid)
     if (a.score == CCO_SCORE_SOFTMAX) {
       s = exp_below(lc, mc);
@@ -288,9 +299,9 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_grad_kernel(RouteArg
       other = lc > 0.0f ? expf(-lc) / (1.0f + expf(-lc)) : 1.0f / (1.0f + expf(lc));
     }
     if (!on) s = 0.0f;
-    const float total = wave_sum(s);
+    const float total = wave_total(s);
     const float q = total == 0.0f ? 0.0f : s / total;
-    const float mean = wave_sum(on ? dw * q : 0.0f);
+    const float mean = wave_total(on ? dw * q : 0.0f);
     part = on ? a.scale * (dw - mean) * q * other : 0.0f;
   } else {
     const float s = lc > 0.0f ? 1.0f / (1.0f + expf(-lc)) : expf(lc) / (1.0f + expf(lc));
@@ -302,8 +313,8 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_grad_kernel(RouteArg
   for (int i = 0; i < EPL; ++i)
     g[i] = (a.score == CCO_SCORE_SOFTMAX && !a.renorm) ? -p[i] * down_all : 0.0f;
   for (int j = 0; j < a.K; ++j) {
-    const int ej = __shfl(id, j, kWave);
-    const float pj = __shfl(part, j, kWave);
+    const int ej = (int)lane_value((uint32_t)id, j);
+    const float pj = lane_value(part, j);
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       if (lane + i * kWave == ej) g[i] += pj;
@@ -317,12 +328,16 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_grad_kernel(RouteArg
 
 template <int DT, int EPL>
 hipError_t launch_route_as(bool grad, const RouteArgs &a, hipStream_t st) {
-  const dim3 grid((uint32_t)(((int64_t)a.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+  // few tokens: a workgroup each, so that they spread over the CUs
+  const int waves = a.T < 4096 ? 1 : kRouteWaves;
+  const dim3 grid((uint32_t)(((int64_t)a.T + waves - 1) / waves)), block(waves * kWave);
   if (grad)
     hipLaunchKernelGGL((route_grad_kernel<DT, EPL>), grid, block, 0, st, a);
+  else if (a.bias || a.groups > 1)
+    hipLaunchKernelGGL((route_kernel<DT, EPL, true>), grid, block,
+                       a.groups > 1 ? (size_t)waves * a.E * sizeof(double) : 0, st, a);
   else
-    hipLaunchKernelGGL((route_kernel<DT, EPL>), grid, block,
-                       a.groups > 1 ? (size_t)kRouteWaves * a.E * sizeof(double) : 0, st, a);
+    hipLaunchKernelGGL((route_kernel<DT, EPL, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
