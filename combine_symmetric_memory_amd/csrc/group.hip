@@ -201,11 +201,15 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
 }
 
 // The fast kernel: tiles of this XCD's contiguous part of the list
-// (workgroup id mod 8 is the XCD), every (gridDim / 8)-th of them.
-template <int OP, bool F16, bool OUT32>
+// (workgroup id mod 8 is the XCD), every (gridDim / 8)-th of them.  A tile's
+// first loads are issued before the previous tile's results are stored.
+// ACC (dw): results are added to what is there.
+template <int OP, bool F16, bool OUT32, bool ACC>
 __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs a) {
   constexpr bool AKC = OP != kGroupDw, BKC = OP == kGroupProduct;
   constexpr int ES = OUT32 ? 4 : 2;
+  using Full = TileShape<AKC, BKC, 256, 256, 3>;
+  using Wide = TileShape<AKC, BKC, 128, 512, 2>;
   extern __shared__ __align__(1024) char smem[];
   // sums in accumulation registers: that form of the MFMAs draws less power
   asm volatile("" ::: "a0");
@@ -217,11 +221,10 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
     map.total = (int64_t)a.groups * mt * nt;
   else
     map.init(a, (int64_t *)smem, [&](int rows) { return row_tile_units(row_tiles(rows, ncol)); });
-  const int xcd = blockIdx.x % kNumXcd;
-  const int64_t end = map.total * (xcd + 1) / kNumXcd;
-  for (int64_t L = map.total * xcd / kNumXcd + blockIdx.x / kNumXcd; L < end;
-       L += gridDim.x / kNumXcd) {
-    GroupTile t;
+
+  GroupTile t;
+  bool wide = false;
+  auto tile_at = [&](int64_t L) __attribute__((always_inline)) {
     int g, r;
     if constexpr (OP == kGroupDw) {
       g = (int)(L / (mt * nt));
@@ -252,10 +255,8 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
       t.c = a.c + (g * welems + (int64_t)row0 * a.k + col0) * ES;
       t.c_rows = min(256, a.n - row0);
       t.c_cols = min(256, a.k - col0);
-      run_group_tile<AKC, BKC, F16, OUT32, 256, 256, 3>(t, smem, a.accumulate != 0);
     } else {
       int row0, col0;
-      bool wide;
       row_tile_at(row_tiles(rows, ncol), r, row0, col0, wide);
       row0 = uniform(row0);
       col0 = uniform(col0);
@@ -263,21 +264,38 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
       t.a_rows = min(256, rows - row0);
       t.kdim = OP == kGroupProduct ? a.k : a.n;
       t.a_cols = t.a_width = 0;
-      const int width = wide ? 512 : 256;
       t.b = a.b + g * welems * 2;
       if (OP == kGroupProduct) t.b += (int64_t)col0 * a.ldb * 2;
-      t.b_rows = min(width, ncol - col0);
+      t.b_rows = min(wide ? 512 : 256, ncol - col0);
       t.b_cols = col0;
       t.b_width = a.k;
       t.ldc = a.ldc * 2;
       t.c = a.c + ((lo + row0) * a.ldc + col0) * 2;
       t.c_rows = t.a_rows;
       t.c_cols = t.b_rows;
-      if (wide)
-        run_group_tile<AKC, BKC, F16, OUT32, 128, 512, 2>(t, smem, false);
-      else
-        run_group_tile<AKC, BKC, F16, OUT32, 256, 256, 3>(t, smem, false);
     }
+    if (OP != kGroupDw && wide)
+      Wide::start(t, smem);
+    else
+      Full::start(t, smem);
+  };
+
+  const int xcd = blockIdx.x % kNumXcd;
+  const int64_t end = map.total * (xcd + 1) / kNumXcd;
+  const int64_t stride = gridDim.x / kNumXcd;
+  int64_t L = map.total * xcd / kNumXcd + blockIdx.x / kNumXcd;
+  if (L >= end) return;
+  tile_at(L);
+  bool stored = false;
+  for (; L < end; L += stride) {
+    const GroupTile now = t;
+    auto next = [&]() __attribute__((always_inline)) {
+      if (L + stride < end) tile_at(L + stride);
+    };
+    if (OP != kGroupDw && wide)
+      stored = run_group_tile<Wide, AKC, BKC, F16, OUT32, ACC, 128, 512, 2>(now, smem, stored, next);
+    else
+      stored = run_group_tile<Full, AKC, BKC, F16, OUT32, ACC, 256, 256, 3>(now, smem, stored, next);
   }
 }
 
@@ -309,8 +327,11 @@ hipError_t launch_tiles(const GroupArgs &a, hipStream_t st) {
   if (tiles == 0) return hipSuccess;
   // whole XCDs
   const int64_t grid = std::min((tiles + kNumXcd - 1) / kNumXcd * kNumXcd, kMaxGrid);
-  hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32>), dim3((uint32_t)grid),
-                     dim3(kGemmWaves * kWave), kGemmLdsBytes, st, a);
+  const dim3 g((uint32_t)grid), b(kGemmWaves * kWave);
+  if (OP == kGroupDw && a.accumulate)
+    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, OP == kGroupDw>), g, b, kGemmLdsBytes, st, a);
+  else
+    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, false>), g, b, kGemmLdsBytes, st, a);
   return hipGetLastError();
 }
 

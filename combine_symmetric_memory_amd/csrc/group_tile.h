@@ -149,27 +149,84 @@ struct TileFrags {
   }
 };
 
-template <bool AKC, bool BKC, bool F16, bool OUT32, int BM, int BN, int RB>
-__device__ __forceinline__ void run_group_tile(const GroupTile &t, char *smem, bool accumulate) {
-  constexpr int WM = BM / 128, WN = kGemmWaves / WM, FM = 4, FN = 4;
+// A tile shape with its rings, and the loads a tile starts with: step 0 of
+// both operands, and step 1 of B where it has three slots.
+template <bool AKC, bool BKC, int BM, int BN, int RB>
+struct TileShape {
+  static constexpr int WM = BM / 128, WN = kGemmWaves / WM;
   using LdA = TileLoads<AKC, BM>;
   using LdB = TileLoads<BKC, BN>;
-  using FrA = TileFrags<AKC, BM, WM>;
-  using FrB = TileFrags<BKC, BN, 1>;
-  constexpr int LA = LdA::N, LB = LdB::N, LPS = LA + LB;
-  constexpr int A_BYTES = LdA::BYTES, B_BYTES = LdB::BYTES, B_OFF = 2 * A_BYTES;
+  static constexpr int LA = LdA::N, LB = LdB::N;
+  static constexpr int A_BYTES = LdA::BYTES, B_BYTES = LdB::BYTES, B_OFF = 2 * A_BYTES;
   static_assert(BM * WN == 128 * kGemmWaves && BN == WN * 128, "128 x 128 per wavefront");
   static_assert(B_OFF + RB * B_BYTES <= kGemmLdsBytes, "the rings must fit the LDS");
   static_assert(RB == 2 || RB == 3, "two or three slots of B");
-  static_assert(LPS < 64, "vmcnt range");
+  static_assert(LA + LB < 64, "vmcnt range");
+  static_assert(B_OFF + (RB - 1) * B_BYTES <= 128 * 1024, "the first loads leave the staging area");
+
+  __device__ static __forceinline__ void init(const GroupTile &t, LdA &la, LdB &lb, int wave,
+                                              int lane) {
+    la.init(t.a, t.lda, t.a_cols, t.a_rows, t.a_width, t.kdim, wave, lane);
+    lb.init(t.b, t.ldb, t.b_cols, t.b_rows, t.b_width, t.kdim, wave, lane);
+  }
+  __device__ static __forceinline__ void start(const GroupTile &t, char *smem) {
+    const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
+    LdA la;
+    LdB lb;
+    init(t, la, lb, wave, lane);
+    const auto a0 = la.step(0);
+    const auto b0 = lb.step(0);
+#pragma unroll
+    for (int q = 0; q < LA; ++q) la.issue(a0, q, smem, wave);
+#pragma unroll
+    for (int q = 0; q < LB; ++q) lb.issue(b0, q, smem + B_OFF, wave);
+    if constexpr (RB == 3) {
+      const auto b1 = lb.step(1);
+#pragma unroll
+      for (int q = 0; q < LB; ++q) lb.issue(b1, q, smem + B_OFF + B_BYTES, wave);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+};
+
+// Lanes 32..63 of a trade places with lanes 0..31 of b.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+// Where the results are staged: the last 32 KiB, which the first loads of no
+// shape fill.
+constexpr int kStageOff = 128 * 1024;
+
+// Stores one wavefront makes of a tile whose four row blocks all exist.
+template <bool OUT32>
+constexpr int kTileStores = 4 * 4 * (OUT32 ? 4 : 2);
+
+// The tile whose first loads `start` has issued.  stored_before: the
+// previous tile of this workgroup left all its kTileStores behind those
+// loads (false: any number).  next(): called once the operands are used up
+// and the rings are idle; it issues the next tile's first loads, which then
+// run while this tile's results are stored.
+template <class Shape, bool AKC, bool BKC, bool F16, bool OUT32, bool ACC, int BM, int BN, int RB,
+          class Next>
+__device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, bool stored_before,
+                                               Next &&next) {
+  constexpr int WM = Shape::WM, WN = Shape::WN, FM = 4, FN = 4;
+  using LdA = typename Shape::LdA;
+  using LdB = typename Shape::LdB;
+  using FrA = TileFrags<AKC, BM, WM>;
+  using FrB = TileFrags<BKC, BN, 1>;
+  constexpr int LA = Shape::LA, LB = Shape::LB, LPS = LA + LB;
+  constexpr int A_BYTES = Shape::A_BYTES, B_BYTES = Shape::B_BYTES, B_OFF = Shape::B_OFF;
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = uniform(tid / kWave);
   const int wm = wave / WN, wn = wave % WN;
   LdA la;
   LdB lb;
-  la.init(t.a, t.lda, t.a_cols, t.a_rows, t.a_width, t.kdim, wave, lane);
-  lb.init(t.b, t.ldb, t.b_cols, t.b_rows, t.b_width, t.kdim, wave, lane);
+  Shape::init(t, la, lb, wave, lane);
   FrA ra;
   FrB rb;
   ra.init(lds_addr(smem), wm, lane);
@@ -273,24 +330,17 @@ __device__ __forceinline__ void run_group_tile(const GroupTile &t, char *smem, b
     constexpr int L3 = LPS / 4, L0 = LPS / 2, L1 = LPS - L3 - L0;
     char *const bring = smem + B_OFF;
 
-    // steps 0 .. RB - 2 of B and step 0 of A in flight; step 0 complete; its
-    // first fragments into buffer 0
-    {
-      const auto a0 = la.step(0);
-      const auto b0 = lb.step(0);
-#pragma unroll
-      for (int q = 0; q < LA; ++q) la.issue(a0, q, smem, wave);
-#pragma unroll
-      for (int q = 0; q < LB; ++q) lb.issue(b0, q, bring, wave);
-      if constexpr (RB == 3) {
-        const auto b1 = lb.step(1);
-#pragma unroll
-        for (int q = 0; q < LB; ++q) lb.issue(b1, q, bring + B_BYTES, wave);
-      }
-      wait_vmcnt<(RB == 3 ? LB : 0)>();
-      stage_barrier();
-      static_for<NRD>([&](auto r_c) __attribute__((always_inline)) { read(I0{}, I0{}, r_c, 0u, 0u); });
-    }
+    // step 0 complete everywhere; its first fragments into buffer 0.  Behind
+    // its loads are those of B's step 1 and the last tile's stores; both
+    // counts are issue counts, and the operations complete in order.
+    constexpr int BEHIND = RB == 3 ? LB : 0;
+    constexpr int STORED = BEHIND + kTileStores<OUT32>;
+    if (stored_before)
+      wait_vmcnt<(STORED < 63 ? STORED : 63)>();
+    else
+      wait_vmcnt<BEHIND>();
+    stage_barrier();
+    static_for<NRD>([&](auto r_c) __attribute__((always_inline)) { read(I0{}, I0{}, r_c, 0u, 0u); });
     // Step kt: A slot AS = kt % 2, B slot bs = kt % RB.  The batch issued
     // after its barrier: A of kt + 2 and B of kt + RB, into the same slots.
     auto step = [&](auto as_c, int kt, int bs) __attribute__((always_inline)) {
@@ -331,99 +381,138 @@ __device__ __forceinline__ void run_group_tile(const GroupTile &t, char *smem, b
     if (kt < nk) step(I0{}, kt, bs);
     wait_lgkmcnt<0>();
     wait_vmcnt<0>();  // the loads past the last step land before the rings are reused
-    __syncthreads();
+    stage_barrier();
+    next();
 
-    // Epilogue through the idle rings, so that rows leave in whole lines:
-    // lane l holds row l % 32 of a block, columns 8 q + 4 (l / 32) + 0..3.
-    // The empty asm keeps the accumulator reads of one block together.
-    if constexpr (OUT32) {
-      // 128 columns of fp32 at a time
-      constexpr int OROWB = 128 * 4 + 16;
-      static_assert(BM * OROWB <= kGemmLdsBytes, "half a tile must fit the LDS");
+    // Results, 32 rows of 256 bytes at a time, through 8 KiB of LDS of this
+    // wavefront's own (past every slot the next tile's first loads fill), so
+    // that a store covers whole 256-byte runs; stored from the registers'
+    // order, 32 bytes a row, the stores took 30 % of the weight gradient's
+    // time.  Lane l holds row l % 32 of a block and columns
+    // 8 q + 4 (l / 32) + 0..3.  Chunk c of row r lies at c ^ (r % 16).
+    // Rows and columns that do not exist are cut off by the buffer's range
+    // (columns by the offset's top bit): every store is issued.
+    constexpr int ES = OUT32 ? 4 : 2;
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4_rw;
+    const uint32_t stage = lds_addr(smem) + kStageOff + wave * 8192;
+    const uint32_t ldc = (uint32_t)uniform((int)t.ldc);
+    const __amdgpu_buffer_rsrc_t rc =
+        byte_range_rsrc(uniform(t.c), (uint32_t)(t.c_rows - 1) * ldc + (uint32_t)t.c_cols * ES);
+    const int r32 = lane & 31, half = lane >> 5;
+    // the chunk this lane stores: row l / 16 of four, columns of chunk l % 16
+    const int srow = lane >> 4, schunk = lane & 15;
+    // fp32 staging (fp32 results, or 16-bit ones that are added to what is
+    // there, which round once): two passes of 64 columns a row block
+    auto stage_f32 = [&](auto i_c, auto pass_c) __attribute__((always_inline)) {
+      constexpr int i = decltype(i_c)::value, pass = decltype(pass_c)::value;
+      static_for<2>([&](auto jj_c) __attribute__((always_inline)) {
+        constexpr int j = pass * 2 + decltype(jj_c)::value;
+        asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
-      for (int h = 0; h < WN; ++h) {
-        if (wn == h)
-          static_for<NACT>([&](auto i_c) __attribute__((always_inline)) {
-            constexpr int i = decltype(i_c)::value;
-            char *orow = smem + ((wm + i * WM) * 32 + (lane & 31)) * OROWB + (lane / 32) * 16;
-            static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
-              constexpr int j = decltype(j_c)::value;
-              asm volatile("" : "+a"(acc[i][j]));
+        for (int q = 0; q < 4; ++q) {
+          f32x4 w;
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                *(float4 *)(orow + j * 128 + q * 32) =
-                    make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                acc[i][j][4 * q + 3]);
-            });
-          });
-        __syncthreads();
-        const int cols = min(128, t.c_cols - h * 128);
-        for (int idx = tid; idx < t.c_rows * 32; idx += kGemmWaves * kWave) {
-          const int row = idx / 32, ch = idx % 32;
-          if (ch * 4 < cols) {
-            float4 v = *(const float4 *)(smem + row * OROWB + ch * 16);
-            float4 *p = (float4 *)(t.c + row * t.ldc + (h * 128 + ch * 4) * 4);
-            if (accumulate) {
-              const float4 o = *p;
-              v.x += o.x;
-              v.y += o.y;
-              v.z += o.z;
-              v.w += o.w;
-            }
-            *p = v;
-          }
+          for (int e = 0; e < 4; ++e) w[e] = acc[i][j][4 * q + e];
+          const int c = decltype(jj_c)::value * 8 + q * 2 + half;
+          *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * 256 + ((c ^ (r32 & 15)) * 16)) =
+              __builtin_bit_cast(u32x4, w);
         }
-        __syncthreads();
-      }
-    } else {
-      constexpr int OROWB = BN * 2 + 16;
-      static_assert(BM * OROWB <= kGemmLdsBytes, "the output tile must fit the LDS");
-      // accumulation adds to what is there before the one rounding, so the
-      // sums meet the old values in registers
-      static_for<NACT>([&](auto i_c) __attribute__((always_inline)) {
-        constexpr int i = decltype(i_c)::value;
-        const int row = (wm + i * WM) * 32 + (lane & 31);
-        char *orow = smem + row * OROWB + (lane / 32) * 8;
-        static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
-          constexpr int j = decltype(j_c)::value;
-          asm volatile("" : "+a"(acc[i][j]));
-          const int col = wn * 128 + j * 32;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = acc[i][j][4 * q + c];
-            if (accumulate) {
-              const int cc = col + q * 8 + (lane / 32) * 4;
-              if (row < t.c_rows && cc < t.c_cols) {
-                const u32x2 o = *(const u32x2 *)(t.c + row * t.ldc + cc * 2);
-                v[0] += from_half_bits<F16>((uint16_t)o.x);
-                v[1] += from_half_bits<F16>((uint16_t)(o.x >> 16));
-                v[2] += from_half_bits<F16>((uint16_t)o.y);
-                v[3] += from_half_bits<F16>((uint16_t)(o.y >> 16));
-              }
-            }
-            u32x2 w;
-            w.x = (uint32_t)to_half_bits<F16>(v[0]) | ((uint32_t)to_half_bits<F16>(v[1]) << 16);
-            w.y = (uint32_t)to_half_bits<F16>(v[2]) | ((uint32_t)to_half_bits<F16>(v[3]) << 16);
-            *(u32x2 *)(orow + (col + q * 8) * 2) = w;
-          }
-        });
       });
-      __syncthreads();
-      constexpr int CHUNKS = BN / 8;
-      for (int idx = tid; idx < t.c_rows * CHUNKS; idx += kGemmWaves * kWave) {
-        const int row = idx / CHUNKS, ch = idx % CHUNKS;
-        if (ch * 8 < t.c_cols)
-          *(u32x4 *)(t.c + row * t.ldc + ch * 16) = *(const u32x4 *)(smem + row * OROWB + ch * 16);
+      const int col = wn * 128 + pass * 64 + schunk * 4;
+      const uint32_t soff = (uint32_t)((wm + i * WM) * 32) * ldc;
+      const uint32_t v0 =
+          ((uint32_t)srow * ldc + (uint32_t)col * ES) | (col < t.c_cols ? 0u : 0x80000000u);
+u32x4 w[8];
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int row = it * 4 + srow;
+        w[it] = *(lds_cu32x4_t *)(uintptr_t)(stage + row * 256 + ((schunk ^ (row & 15)) * 16));
       }
-      __syncthreads();
-    }
+      if constexpr (OUT32) {
+        if constexpr (ACC) {
+          u32x4 o[8];
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            o[it] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+                                                          (int)soff, 0);
+#pragma unroll
+          for (int it = 0; it < 8; ++it)
+            w[it] = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, w[it]) +
+                                                  __builtin_bit_cast(f32x4, o[it]));
+        }
+#pragma unroll
+        for (int it = 0; it < 8; ++it)
+          __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+                                                 (int)soff, 0);
+      } else {
+        u32x2 o[8];
+#pragma unroll
+        for (int it = 0; it < 8; ++it)
+          o[it] = __builtin_amdgcn_raw_buffer_load_b64(rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+                                                       (int)soff, 0);
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+          const f32x4 f = __builtin_bit_cast(f32x4, w[it]);
+          const uint32_t o0 = o[it].x, o1 = o[it].y;
+          u32x2 d;
+          d.x = (uint32_t)to_half_bits<F16>(f[0] + from_half_bits<F16>((uint16_t)o0)) |
+                ((uint32_t)to_half_bits<F16>(f[1] + from_half_bits<F16>((uint16_t)(o0 >> 16))) << 16);
+          d.y = (uint32_t)to_half_bits<F16>(f[2] + from_half_bits<F16>((uint16_t)o1)) |
+                ((uint32_t)to_half_bits<F16>(f[3] + from_half_bits<F16>((uint16_t)(o1 >> 16))) << 16);
+          __builtin_amdgcn_raw_buffer_store_b64(d, rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+                                                (int)soff, 0);
+        }
+      }
+    };
+    auto stage_half = [&](auto i_c) __attribute__((always_inline)) {
+      constexpr int i = decltype(i_c)::value;
+      static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
+        constexpr int j = decltype(j_c)::value;
+        asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {  // columns 16 q ..
+          uint32_t d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            d[e] = (uint32_t)to_half_bits<F16>(acc[i][j][8 * q + 2 * e]) |
+                   ((uint32_t)to_half_bits<F16>(acc[i][j][8 * q + 2 * e + 1]) << 16);
+          // lanes l and l ^ 32 trade halves: eight columns a lane
+          swap_halves(d[0], d[2]);
+          swap_halves(d[1], d[3]);
+          const int c = j * 4 + q * 2 + half;
+          *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * 256 + ((c ^ (r32 & 15)) * 16)) =
+              u32x4{d[0], d[1], d[2], d[3]};
+        }
+      });
+      const int col = wn * 128 + schunk * 8;
+      const uint32_t soff = (uint32_t)((wm + i * WM) * 32) * ldc;
+      const uint32_t v0 =
+          ((uint32_t)srow * ldc + (uint32_t)col * 2) | (col < t.c_cols ? 0u : 0x80000000u);
+      u32x4 w[8];
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int row = it * 4 + srow;
+        w[it] = *(lds_cu32x4_t *)(uintptr_t)(stage + row * 256 + ((schunk ^ (row & 15)) * 16));
+      }
+#pragma unroll
+      for (int it = 0; it < 8; ++it)
+        __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+                                               (int)soff, 0);
+    };
+    if constexpr (OUT32 || ACC)
+      static_for<NACT>([&](auto i_c) __attribute__((always_inline)) {
+        stage_f32(i_c, I0{});
+        stage_f32(i_c, I1{});
+      });
+    else
+      static_for<NACT>([&](auto i_c) __attribute__((always_inline)) { stage_half(i_c); });
+    __builtin_amdgcn_sched_barrier(0);
   };
   // one specialisation per count of active row blocks (wavefront-uniform)
   static_for<FM + 1>([&](auto c) __attribute__((always_inline)) {
     if (nact == decltype(c)::value) k_loop(c);
   });
+  return nact == FM;
 }
 
 // ------------------------------------------------------- the tile lists --
