@@ -30,8 +30,6 @@
 namespace cco {
 namespace {
 
-constexpr int kNumCus = 256;
-
 // Eight elements as they lie in memory (16-bit types 16 bytes, fp32 32).
 // Rows and vectors may be aligned to an element only: the loads are
 // unaligned 16-byte ones, which cost nothing where the address is aligned.

@@ -203,24 +203,31 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
 // The fast kernel: tiles of this XCD's contiguous part of the list
 // (workgroup id mod 8 is the XCD), every (gridDim / 8)-th of them.  A tile's
 // first loads are issued before the previous tile's results are stored.
-// ACC (dw): results are added to what is there.
-template <int OP, bool F16, bool OUT32, bool ACC>
-__global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs a) {
-  constexpr bool AKC = OP != kGroupDw, BKC = OP == kGroupProduct;
+// ACC (dw): results are added to what is there.  TILE: 256, or 128 with two
+// workgroups on a CU.
+template <int OP, int TILE>
+using FullTile = TileShape<OP != kGroupDw, OP == kGroupProduct, TILE, TILE, 3, TILE / 64>;
+template <int OP>
+using WideTile = TileShape<OP != kGroupDw, OP == kGroupProduct, 128, 512, 2, 4>;
+
+template <int OP, bool F16, bool OUT32, bool ACC, int TILE>
+__global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_tile_kernel(
+    GroupArgs a) {
   constexpr int ES = OUT32 ? 4 : 2;
-  using Full = TileShape<AKC, BKC, 256, 256, 3>;
-  using Wide = TileShape<AKC, BKC, 128, 512, 2>;
+  using Full = FullTile<OP, TILE>;
+  using Wide = WideTile<OP>;
+  constexpr bool WIDE = OP != kGroupDw && TILE == 256;
   extern __shared__ __align__(1024) char smem[];
   // sums in accumulation registers: that form of the MFMAs draws less power
   asm volatile("" ::: "a0");
   const int ncol = OP == kGroupProduct ? a.n : a.k;
   const int64_t welems = (int64_t)a.n * a.k;
-  const int mt = (a.n + 255) / 256, nt = (ncol + 255) / 256;  // dw: tiles of a group
+  const int mt = (a.n + TILE - 1) / TILE, nt = (ncol + TILE - 1) / TILE;  // dw: tiles of a group
   TileMap<kGemmWaves * kWave> map;
   if constexpr (OP == kGroupDw)
     map.total = (int64_t)a.groups * mt * nt;
   else
-    map.init(a, (int64_t *)smem, [&](int rows) { return row_tile_units(row_tiles(rows, ncol)); });
+    map.init(a, (int64_t *)smem, [&](int rows) { return row_tile_units(row_tiles<TILE>(rows, ncol)); });
 
   GroupTile t;
   bool wide = false;
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
       // XCD share about eight panels of dy and four of x
       const int band = r / (mt * 4), bw = min(4, nt - band * 4);
       const int rr = r - band * mt * 4;
-      const int row0 = rr / bw * 256, col0 = (band * 4 + rr % bw) * 256;
+      const int row0 = rr / bw * TILE, col0 = (band * 4 + rr % bw) * TILE;
       t.a = a.a + lo * a.lda * 2;
       t.b = a.b + lo * a.ldb * 2;
       t.a_cols = row0;
@@ -253,20 +260,20 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
       t.kdim = rows;
       t.ldc = (int64_t)a.k * ES;
       t.c = a.c + (g * welems + (int64_t)row0 * a.k + col0) * ES;
-      t.c_rows = min(256, a.n - row0);
-      t.c_cols = min(256, a.k - col0);
+      t.c_rows = min(TILE, a.n - row0);
+      t.c_cols = min(TILE, a.k - col0);
     } else {
       int row0, col0;
-      row_tile_at(row_tiles(rows, ncol), r, row0, col0, wide);
+      row_tile_at<TILE>(row_tiles<TILE>(rows, ncol), r, row0, col0, wide);
       row0 = uniform(row0);
       col0 = uniform(col0);
       t.a = a.a + (lo + row0) * a.lda * 2;
-      t.a_rows = min(256, rows - row0);
+      t.a_rows = min(TILE, rows - row0);
       t.kdim = OP == kGroupProduct ? a.k : a.n;
       t.a_cols = t.a_width = 0;
       t.b = a.b + g * welems * 2;
       if (OP == kGroupProduct) t.b += (int64_t)col0 * a.ldb * 2;
-      t.b_rows = min(wide ? 512 : 256, ncol - col0);
+      t.b_rows = min(wide ? 512 : TILE, ncol - col0);
       t.b_cols = col0;
       t.b_width = a.k;
       t.ldc = a.ldc * 2;
@@ -274,10 +281,12 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
       t.c_rows = t.a_rows;
       t.c_cols = t.b_rows;
     }
-    if (OP != kGroupDw && wide)
-      Wide::start(t, smem);
-    else
-      Full::start(t, smem);
+    if constexpr (WIDE)
+      if (wide) {
+        Wide::start(t, smem);
+        return;
+      }
+    Full::start(t, smem);
   };
 
   const int xcd = blockIdx.x % kNumXcd;
@@ -292,10 +301,12 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
     auto next = [&]() __attribute__((always_inline)) {
       if (L + stride < end) tile_at(L + stride);
     };
-    if (OP != kGroupDw && wide)
-      stored = run_group_tile<Wide, AKC, BKC, F16, OUT32, ACC, 128, 512, 2>(now, smem, stored, next);
-    else
-      stored = run_group_tile<Full, AKC, BKC, F16, OUT32, ACC, 256, 256, 3>(now, smem, stored, next);
+    if constexpr (WIDE)
+      if (wide) {
+        stored = run_group_tile<Wide, F16, OUT32, ACC>(now, smem, stored, next);
+        continue;
+      }
+    stored = run_group_tile<Full, F16, OUT32, ACC>(now, smem, stored, next);
   }
 }
 
@@ -303,41 +314,63 @@ __global__ __launch_bounds__(kGemmWaves *kWave) void group_tile_kernel(GroupArgs
 // uneven tiles; the kernels take further tiles in a loop.
 constexpr int64_t kMaxGrid = 4096;
 
+// Upper bound of the tiles of a call.  Rows of a group: at most one partly
+// filled row of tiles for every group with rows.
+template <int OP, int TILE>
+int64_t tile_bound(const GroupArgs &a) {
+  const int64_t ncol = OP == kGroupProduct ? a.n : a.k, ct = (ncol + TILE - 1) / TILE;
+  return OP == kGroupDw ? (int64_t)a.groups * ct * ((a.n + TILE - 1) / TILE)
+                        : (a.rows / TILE + std::min<int64_t>(a.groups, a.rows)) * ct;
+}
+
+// Tiles of 128 where those of 256 (counted as if the rows were spread evenly
+// over the groups) would leave a third of the CUs idle: 128 tiles of 256 ran
+// 93 us and as tiles of 128 68 us (1 group, 4096 x 2048 x 4096, dw), 116 of
+// them 78 and 54 us, but 196 of them 51 and 58 us, and 256 of them 113 and
+// 141 us (8 groups, 4096 x 4096 x 4096, product).
+template <int OP>
+bool small_tiles(const GroupArgs &a) {
+  int64_t tiles;
+  if (OP == kGroupDw) {
+    tiles = tile_bound<OP, 256>(a);
+  } else {
+    const int64_t ct = ((OP == kGroupProduct ? a.n : a.k) + 255) / 256;
+    const int64_t g = std::max<int64_t>(1, std::min<int64_t>(a.groups, a.rows));
+    const int64_t avg = (a.rows + g - 1) / g, rem = avg % 256;
+    tiles = g * (avg / 256 * ct + (rem == 0 ? 0 : (rem <= 128 ? (ct + 1) / 2 : ct)));
+  }
+  return 3 * tiles < 2 * kNumCus;
+}
+
 template <int OP, bool F16, bool OUT32>
 hipError_t launch_general(const GroupArgs &a, hipStream_t st) {
-  const int64_t ncol = OP == kGroupProduct ? a.n : a.k;
-  const int64_t ct = (ncol + kGenTile - 1) / kGenTile;
-  int64_t tiles;
-  if (OP == kGroupDw)
-    tiles = (int64_t)a.groups * ct * ((a.n + kGenTile - 1) / kGenTile);
-  else  // every group with rows has at most one partly filled row of tiles
-    tiles = (a.rows / kGenTile + std::min<int64_t>(a.groups, a.rows)) * ct;
+  const int64_t tiles = tile_bound<OP, kGenTile>(a);
   if (tiles == 0) return hipSuccess;
   hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32>),
                      dim3((uint32_t)std::min(tiles, kMaxGrid)), dim3(kGenThreads), 0, st, a);
   return hipGetLastError();
 }
 
-template <int OP, bool F16, bool OUT32>
+template <int OP, bool F16, bool OUT32, int TILE>
 hipError_t launch_tiles(const GroupArgs &a, hipStream_t st) {
-  const int64_t ncol = OP == kGroupProduct ? a.n : a.k, ct = (ncol + 255) / 256;
-  const int64_t tiles = OP == kGroupDw
-                            ? (int64_t)a.groups * ct * ((a.n + 255) / 256)
-                            : (a.rows / 256 + std::min<int64_t>(a.groups, a.rows)) * ct;
+  const int64_t tiles = tile_bound<OP, TILE>(a);
   if (tiles == 0) return hipSuccess;
   // whole XCDs
   const int64_t grid = std::min((tiles + kNumXcd - 1) / kNumXcd * kNumXcd, kMaxGrid);
   const dim3 g((uint32_t)grid), b(kGemmWaves * kWave);
+  constexpr int lds = FullTile<OP, TILE>::LDS_BYTES;
   if (OP == kGroupDw && a.accumulate)
-    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, OP == kGroupDw>), g, b, kGemmLdsBytes, st, a);
+    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, OP == kGroupDw, TILE>), g, b, lds, st, a);
   else
-    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, false>), g, b, kGemmLdsBytes, st, a);
+    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, false, TILE>), g, b, lds, st, a);
   return hipGetLastError();
 }
 
 template <int OP, bool F16, bool OUT32>
 hipError_t launch_either(bool aligned, const GroupArgs &a, hipStream_t st) {
-  return aligned ? launch_tiles<OP, F16, OUT32>(a, st) : launch_general<OP, F16, OUT32>(a, st);
+  if (!aligned) return launch_general<OP, F16, OUT32>(a, st);
+  return small_tiles<OP>(a) ? launch_tiles<OP, F16, OUT32, 128>(a, st)
+                            : launch_tiles<OP, F16, OUT32, 256>(a, st);
 }
 
 template <int OP>

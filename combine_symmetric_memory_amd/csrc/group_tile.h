@@ -7,6 +7,10 @@
 // MFMAs' time covers (two wavefronts per SIMD with half the block each would
 // read 12 KiB).  Full tile 256 x 256; the last rows of a group, if at most
 // 128, take a 128 x 512 tile, so that few rows do not cost a whole tile.
+// Where 256 x 256 tiles would be few, or end after a few reduction steps,
+// tiles of 128 x 128 (2 x 2 blocks a wavefront) with two workgroups on a CU:
+// four times the tiles, and one workgroup's stores and first loads run while
+// the other multiplies.
 //
 // Operands go global -> LDS by direct 16-byte loads into two rings of
 // reduction steps of 64: two slots of A and three of B (the weights, or x in
@@ -151,18 +155,26 @@ struct TileFrags {
 
 // A tile shape with its rings, and the loads a tile starts with: step 0 of
 // both operands, and step 1 of B where it has three slots.
-template <bool AKC, bool BKC, int BM, int BN, int RB>
+// RB slots of B; each wavefront has FB x FB blocks of 32 x 32.
+template <bool AKC_, bool BKC_, int BM_, int BN_, int RB_, int FB_>
 struct TileShape {
-  static constexpr int WM = BM / 128, WN = kGemmWaves / WM;
+  static constexpr bool AKC = AKC_, BKC = BKC_;
+  static constexpr int BM = BM_, BN = BN_, RB = RB_, FB = FB_;
+  static constexpr int WM = BM / (32 * FB), WN = kGemmWaves / WM;
   using LdA = TileLoads<AKC, BM>;
   using LdB = TileLoads<BKC, BN>;
   static constexpr int LA = LdA::N, LB = LdB::N;
   static constexpr int A_BYTES = LdA::BYTES, B_BYTES = LdB::BYTES, B_OFF = 2 * A_BYTES;
-  static_assert(BM * WN == 128 * kGemmWaves && BN == WN * 128, "128 x 128 per wavefront");
-  static_assert(B_OFF + RB * B_BYTES <= kGemmLdsBytes, "the rings must fit the LDS");
+  static constexpr int LDS_BYTES = B_OFF + RB * B_BYTES;
+  // Where results are staged: 32 rows of FB * 64 bytes for every wavefront,
+  // at the rings' end, which the first loads of no shape of its kernel fill.
+  static constexpr int STAGE_ROW = FB * 64, STAGE_BYTES = 32 * STAGE_ROW;
+  static constexpr int STAGE_OFF = LDS_BYTES - kGemmWaves * STAGE_BYTES;
+  static_assert(BN == WN * 32 * FB && WM * WN == kGemmWaves, "the wavefronts' blocks");
+  static_assert(LDS_BYTES <= kGemmLdsBytes, "the rings must fit the LDS");
   static_assert(RB == 2 || RB == 3, "two or three slots of B");
   static_assert(LA + LB < 64, "vmcnt range");
-  static_assert(B_OFF + (RB - 1) * B_BYTES <= 128 * 1024, "the first loads leave the staging area");
+  static_assert(B_OFF + (RB - 1) * B_BYTES <= STAGE_OFF, "the first loads leave the staging area");
 
   __device__ static __forceinline__ void init(const GroupTile &t, LdA &la, LdB &lb, int wave,
                                               int lane) {
@@ -196,28 +208,24 @@ __device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b) {
   b = r[1];
 }
 
-// Where the results are staged: the last 32 KiB, which the first loads of no
-// shape fill.
-constexpr int kStageOff = 128 * 1024;
-
-// Stores one wavefront makes of a tile whose four row blocks all exist.
-template <bool OUT32>
-constexpr int kTileStores = 4 * 4 * (OUT32 ? 4 : 2);
+// Stores one wavefront makes of a tile whose row blocks all exist.
+template <class Shape, bool OUT32>
+constexpr int kTileStores = Shape::FB * Shape::FB * (OUT32 ? 4 : 2);
 
 // The tile whose first loads `start` has issued.  stored_before: the
 // previous tile of this workgroup left all its kTileStores behind those
 // loads (false: any number).  next(): called once the operands are used up
 // and the rings are idle; it issues the next tile's first loads, which then
 // run while this tile's results are stored.
-template <class Shape, bool AKC, bool BKC, bool F16, bool OUT32, bool ACC, int BM, int BN, int RB,
-          class Next>
+template <class Shape, bool F16, bool OUT32, bool ACC, class Next>
 __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, bool stored_before,
                                                Next &&next) {
-  constexpr int WM = Shape::WM, WN = Shape::WN, FM = 4, FN = 4;
+  constexpr int WM = Shape::WM, WN = Shape::WN, FM = Shape::FB, FN = Shape::FB;
+  constexpr int RB = Shape::RB;
   using LdA = typename Shape::LdA;
   using LdB = typename Shape::LdB;
-  using FrA = TileFrags<AKC, BM, WM>;
-  using FrB = TileFrags<BKC, BN, 1>;
+  using FrA = TileFrags<Shape::AKC, Shape::BM, WM>;
+  using FrB = TileFrags<Shape::BKC, Shape::BN, 1>;
   constexpr int LA = Shape::LA, LB = Shape::LB, LPS = LA + LB;
   constexpr int A_BYTES = Shape::A_BYTES, B_BYTES = Shape::B_BYTES, B_OFF = Shape::B_OFF;
 
@@ -230,7 +238,7 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
   FrA ra;
   FrB rb;
   ra.init(lds_addr(smem), wm, lane);
-  rb.init(lds_addr(smem) + B_OFF, wn * 4, lane);
+  rb.init(lds_addr(smem) + B_OFF, wn * FN, lane);
   const int64_t steps = (t.kdim + 63) / 64;
   const int nk = uniform((int)(steps > 0 ? steps : 1));  // no rows: one step of zeros
   const int mblocks = (t.c_rows + 31) / 32;
@@ -334,7 +342,7 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
     // its loads are those of B's step 1 and the last tile's stores; both
     // counts are issue counts, and the operations complete in order.
     constexpr int BEHIND = RB == 3 ? LB : 0;
-    constexpr int STORED = BEHIND + kTileStores<OUT32>;
+    constexpr int STORED = BEHIND + kTileStores<Shape, OUT32>;
     if (stored_before)
       wait_vmcnt<(STORED < 63 ? STORED : 63)>();
     else
@@ -384,29 +392,30 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
     stage_barrier();
     next();
 
-    // Results, 32 rows of 256 bytes at a time, through 8 KiB of LDS of this
-    // wavefront's own (past every slot the next tile's first loads fill), so
-    // that a store covers whole 256-byte runs; stored from the registers'
-    // order, 32 bytes a row, the stores took 30 % of the weight gradient's
-    // time.  Lane l holds row l % 32 of a block and columns
-    // 8 q + 4 (l / 32) + 0..3.  Chunk c of row r lies at c ^ (r % 16).
+    // Results, 32 rows of STAGE_ROW bytes at a time, through a piece of LDS
+    // of this wavefront's own (past every slot the next tile's first loads
+    // fill), so that a store covers whole lines of a row.  Lane l holds row
+    // l % 32 of a block and columns 8 q + 4 (l / 32) + 0..3.  Chunk c of
+    // staged row r lies at c ^ (r % chunks).
     // Rows and columns that do not exist are cut off by the buffer's range
     // (columns by the offset's top bit): every store is issued.
     constexpr int ES = OUT32 ? 4 : 2;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4_rw;
-    const uint32_t stage = lds_addr(smem) + kStageOff + wave * 8192;
+    constexpr int SROW = Shape::STAGE_ROW, CH = SROW / 16;  // bytes and chunks of a row
+    constexpr int RPS = kWave / CH, ITS = 32 / RPS;          // rows a store, stores
+    const uint32_t stage = lds_addr(smem) + Shape::STAGE_OFF + wave * Shape::STAGE_BYTES;
     const uint32_t ldc = (uint32_t)uniform((int)t.ldc);
     const __amdgpu_buffer_rsrc_t rc =
         byte_range_rsrc(uniform(t.c), (uint32_t)(t.c_rows - 1) * ldc + (uint32_t)t.c_cols * ES);
     const int r32 = lane & 31, half = lane >> 5;
-    // the chunk this lane stores: row l / 16 of four, columns of chunk l % 16
-    const int srow = lane >> 4, schunk = lane & 15;
+    // the chunk this lane stores
+    const int srow = lane / CH, schunk = lane % CH;
     // fp32 staging (fp32 results, or 16-bit ones that are added to what is
-    // there, which round once): two passes of 64 columns a row block
+    // there, which round once): two passes a row block, of FN / 2 blocks
     auto stage_f32 = [&](auto i_c, auto pass_c) __attribute__((always_inline)) {
       constexpr int i = decltype(i_c)::value, pass = decltype(pass_c)::value;
-      static_for<2>([&](auto jj_c) __attribute__((always_inline)) {
-        constexpr int j = pass * 2 + decltype(jj_c)::value;
+      static_for<FN / 2>([&](auto jj_c) __attribute__((always_inline)) {
+        constexpr int j = pass * (FN / 2) + decltype(jj_c)::value;
         asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -414,44 +423,44 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[e] = acc[i][j][4 * q + e];
           const int c = decltype(jj_c)::value * 8 + q * 2 + half;
-          *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * 256 + ((c ^ (r32 & 15)) * 16)) =
+          *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * SROW + ((c ^ (r32 % CH)) * 16)) =
               __builtin_bit_cast(u32x4, w);
         }
       });
-      const int col = wn * 128 + pass * 64 + schunk * 4;
+      const int col = wn * FN * 32 + pass * FN * 16 + schunk * 4;
       const uint32_t soff = (uint32_t)((wm + i * WM) * 32) * ldc;
       const uint32_t v0 =
           ((uint32_t)srow * ldc + (uint32_t)col * ES) | (col < t.c_cols ? 0u : 0x80000000u);
-u32x4 w[8];
+      u32x4 w[ITS];
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int row = it * 4 + srow;
-        w[it] = *(lds_cu32x4_t *)(uintptr_t)(stage + row * 256 + ((schunk ^ (row & 15)) * 16));
+      for (int it = 0; it < ITS; ++it) {
+        const int row = it * RPS + srow;
+        w[it] = *(lds_cu32x4_t *)(uintptr_t)(stage + row * SROW + ((schunk ^ (row % CH)) * 16));
       }
       if constexpr (OUT32) {
         if constexpr (ACC) {
-          u32x4 o[8];
+          u32x4 o[ITS];
 #pragma unroll
-          for (int it = 0; it < 8; ++it)
-            o[it] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+          for (int it = 0; it < ITS; ++it)
+            o[it] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
                                                           (int)soff, 0);
 #pragma unroll
-          for (int it = 0; it < 8; ++it)
+          for (int it = 0; it < ITS; ++it)
             w[it] = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, w[it]) +
                                                   __builtin_bit_cast(f32x4, o[it]));
         }
 #pragma unroll
-        for (int it = 0; it < 8; ++it)
-          __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+        for (int it = 0; it < ITS; ++it)
+          __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
                                                  (int)soff, 0);
       } else {
-        u32x2 o[8];
+        u32x2 o[ITS];
 #pragma unroll
-        for (int it = 0; it < 8; ++it)
-          o[it] = __builtin_amdgcn_raw_buffer_load_b64(rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+        for (int it = 0; it < ITS; ++it)
+          o[it] = __builtin_amdgcn_raw_buffer_load_b64(rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
                                                        (int)soff, 0);
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
+        for (int it = 0; it < ITS; ++it) {
           const f32x4 f = __builtin_bit_cast(f32x4, w[it]);
           const uint32_t o0 = o[it].x, o1 = o[it].y;
           u32x2 d;
@@ -459,7 +468,7 @@ u32x4 w[8];
                 ((uint32_t)to_half_bits<F16>(f[1] + from_half_bits<F16>((uint16_t)(o0 >> 16))) << 16);
           d.y = (uint32_t)to_half_bits<F16>(f[2] + from_half_bits<F16>((uint16_t)o1)) |
                 ((uint32_t)to_half_bits<F16>(f[3] + from_half_bits<F16>((uint16_t)(o1 >> 16))) << 16);
-          __builtin_amdgcn_raw_buffer_store_b64(d, rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+          __builtin_amdgcn_raw_buffer_store_b64(d, rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
                                                 (int)soff, 0);
         }
       }
@@ -480,23 +489,23 @@ u32x4 w[8];
           swap_halves(d[0], d[2]);
           swap_halves(d[1], d[3]);
           const int c = j * 4 + q * 2 + half;
-          *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * 256 + ((c ^ (r32 & 15)) * 16)) =
+          *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * SROW + ((c ^ (r32 % CH)) * 16)) =
               u32x4{d[0], d[1], d[2], d[3]};
         }
       });
-      const int col = wn * 128 + schunk * 8;
+      const int col = wn * FN * 32 + schunk * 8;
       const uint32_t soff = (uint32_t)((wm + i * WM) * 32) * ldc;
       const uint32_t v0 =
           ((uint32_t)srow * ldc + (uint32_t)col * 2) | (col < t.c_cols ? 0u : 0x80000000u);
-      u32x4 w[8];
+      u32x4 w[ITS];
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int row = it * 4 + srow;
-        w[it] = *(lds_cu32x4_t *)(uintptr_t)(stage + row * 256 + ((schunk ^ (row & 15)) * 16));
+      for (int it = 0; it < ITS; ++it) {
+        const int row = it * RPS + srow;
+        w[it] = *(lds_cu32x4_t *)(uintptr_t)(stage + row * SROW + ((schunk ^ (row % CH)) * 16));
       }
 #pragma unroll
-      for (int it = 0; it < 8; ++it)
-        __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * 4) * ldc),
+      for (int it = 0; it < ITS; ++it)
+        __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
                                                (int)soff, 0);
     };
     if constexpr (OUT32 || ACC)
@@ -516,22 +525,24 @@ u32x4 w[8];
 }
 
 // ------------------------------------------------------- the tile lists --
-// Rows of a group in the product and dx: q = rows / 256 full tiles of rows
-// and a remainder, which is one more full tile or, if at most 128 rows, a
-// wide tile (when there is more than one column tile).  Bands of 8 row
-// tiles, column-major inside a band, so that the workgroups of one XCD,
-// which take neighbouring tiles, share a few row panels and a few column
-// panels in its L2.  In the last band the wide tile of a column pair stands
-// before the full tiles of the same columns.
+// Rows of a group in the product and dx, TILE rows and columns a tile:
+// q = rows / TILE full tiles of rows and a remainder, which is one more full
+// tile or, with tiles of 256 and at most 128 rows left, a wide tile (when
+// there is more than one column tile).  Bands of 8 row tiles, column-major
+// inside a band, so that the workgroups of one XCD, which take neighbouring
+// tiles, share a few row panels and a few column panels in its L2.  In the
+// last band the wide tile of a column pair stands before the full tiles of
+// the same columns.
 constexpr int kBand = 8;
 struct RowTiles {
   int full, rem_half, ntl, nwide, bands;
 };
+template <int TILE>
 __device__ __forceinline__ RowTiles row_tiles(int rows, int ncol) {
   RowTiles t;
-  t.ntl = (ncol + 255) / 256;
-  const int q = rows / 256, rem = rows % 256;
-  const bool half = rem > 0 && rem <= 128 && t.ntl > 1;
+  t.ntl = (ncol + TILE - 1) / TILE;
+  const int q = rows / TILE, rem = rows % TILE;
+  const bool half = TILE == 256 && rem > 0 && rem <= 128 && t.ntl > 1;
   t.full = q + (rem > 0 && !half);
   t.rem_half = half ? rem : 0;
   t.nwide = half ? (t.ntl + 1) / 2 : 0;
@@ -541,6 +552,7 @@ __device__ __forceinline__ RowTiles row_tiles(int rows, int ncol) {
 __device__ __forceinline__ int row_tile_units(const RowTiles &t) { return t.full * t.ntl + t.nwide; }
 
 // Unit r: its first row, first column, and whether it is a wide tile.
+template <int TILE>
 __device__ __forceinline__ void row_tile_at(const RowTiles &t, int r, int &row0, int &col0,
                                             bool &wide) {
   const int band = min(r / (kBand * t.ntl), t.bands - 1);
@@ -548,12 +560,12 @@ __device__ __forceinline__ void row_tile_at(const RowTiles &t, int r, int &row0,
   const int qb = min(kBand, t.full - band * kBand);
   wide = false;
   int m, n;
-  if (band == t.bands - 1 && t.rem_half) {
+  if (TILE == 256 && band == t.bands - 1 && t.rem_half) {
     const int per = 2 * qb + 1, j = r / per, rr = r - j * per;
     if (rr == 0) {
       wide = true;
-      row0 = t.full * 256;
-      col0 = j * 512;
+      row0 = t.full * TILE;
+      col0 = j * 2 * TILE;
       return;
     }
     n = 2 * j + (rr - 1) / qb;
@@ -562,8 +574,8 @@ __device__ __forceinline__ void row_tile_at(const RowTiles &t, int r, int &row0,
     n = r / qb;
     m = r % qb;
   }
-  row0 = (band * kBand + m) * 256;
-  col0 = n * 256;
+  row0 = (band * kBand + m) * TILE;
+  col0 = n * TILE;
 }
 
 }  // namespace

@@ -12,6 +12,7 @@
 
 namespace cco {
 
+constexpr int kNumCus = 256;          // compute units of one MI355X
 constexpr int kMaxGroups = 1024;      // groups of a grouped product
 constexpr int kMaxRouteGroups = 64;   // groups of experts in the router
 constexpr int kMaxNormHidden = 16384; // a row stays in one workgroup's registers
