@@ -242,6 +242,7 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
     const GroupRows gr = group_rows(a, g);
     const int rows = uniform(gr.n);
     const int64_t lo = gr.lo;
+    t.rot = 0;
     t.lda = (uint32_t)(a.lda * 2);
     t.ldb = (uint32_t)(a.ldb * 2);
     if constexpr (OP == kGroupDw) {
@@ -271,6 +272,8 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
       t.a_rows = min(TILE, rows - row0);
       t.kdim = OP == kGroupProduct ? a.k : a.n;
       t.a_cols = t.a_width = 0;
+      if (OP == kGroupProduct && a.k % 2048 == 0 && a.rows <= 256 * (int64_t)a.groups)
+        t.rot = uniform((col0 / TILE + 3 * g) % (a.k / 64));
       t.b = a.b + g * welems * 2;
       if (OP == kGroupProduct) t.b += (int64_t)col0 * a.ldb * 2;
       t.b_rows = min(wide ? 512 : TILE, ncol - col0);

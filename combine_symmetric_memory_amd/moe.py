@@ -83,6 +83,22 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "
     return ctypes.c_void_p(t.data_ptr())
 
 
+class _DeviceMemory:
+    """Device memory as the array interface torch takes tensors from."""
+
+    def __init__(self, ptr: int, shape: tuple, typestr: str):
+        self.__cuda_array_interface__ = {"data": (ptr, False), "shape": shape, "version": 2,
+                                         "typestr": typestr}
+
+
+def _device_tensor(ptr: int, shape: tuple, typestr: str, device: int) -> torch.Tensor:
+    if 0 in shape:
+        dtype = {"<i2": torch.int16, "<i4": torch.int32}[typestr]
+        return torch.empty(shape, dtype=dtype, device="cuda:%d" % device)
+    with torch.cuda.device(device):
+        return torch.as_tensor(_DeviceMemory(ptr, shape, typestr), device="cuda:%d" % device)
+
+
 class SymHeap:
     """One flat device buffer of `nslots` slots (cco_sym_heap_create)."""
 
@@ -305,6 +321,29 @@ class MoE:
     def combine_in_view(self, slot: int) -> int:
         """Device address of slot's combine staging window."""
         return lib.cco_moe_combine_in_view(self.handle, int(slot))
+
+    def window(self, name: str, slot: int, rows: int) -> torch.Tensor:
+        """The first `rows` rows of a slot's window as a bf16 tensor over the
+        window's own memory (no copy): 'disp_x', 'hbuf' or 'out_tok'.
+        Borrowed: valid until the heap is destroyed."""
+        width = {"disp_x": self.H, "hbuf": self.I, "out_tok": self.H}
+        if name not in width or getattr(self.layout, name + "_bytes") == 0:
+            raise ValueError("no window %r in this layer" % name)
+        if not 0 <= rows <= self.cap or not 0 <= slot < self.S:
+            raise ValueError("slot or rows out of range")
+        ptr = self.heap.slot_ptr(slot, getattr(self.layout, name))
+        return _device_tensor(ptr, (rows, width[name]), "<i2", self.heap.device).view(
+            torch.bfloat16)
+
+    def expert_groups(self, slot: int) -> tuple[torch.Tensor, torch.Tensor]:
+        """(first, count) int32 [E / S] of the slot's experts: the routing
+        state's own memory, the groups of group_product on the slot's rows."""
+        if not 0 <= slot < self.S:
+            raise ValueError("slot out of range")
+        self.handle
+        r, at = self.routing_ptrs, slot * self.eps * 4
+        return (_device_tensor(r.expert_off + at, (self.eps,), "<i4", self.heap.device),
+                _device_tensor(r.counts + at, (self.eps,), "<i4", self.heap.device))
 
     # ----------------------------------------------------- host readback --
     def read_routing(self):
