@@ -21,32 +21,16 @@ namespace {
 constexpr int kGenTile = 128, kGenThreads = 256, kGenStep = 64;
 constexpr int kGenOperand = kGenTile * kGenStep * 2;  // bytes of one operand's step
 
-// Eight elements from column c of row r of a [nr][nc] matrix, zeros outside.
-__device__ __forceinline__ u32x4 load8(const char *base, int64_t ld, int64_t r, int c, int64_t nr,
-                                       int nc) {
-  u32x4 v = {0, 0, 0, 0};
-  if (r < nr && c < nc) {
-    const char *p = base + (r * ld + c) * 2;
-    if (c + 8 <= nc) {
-      __builtin_memcpy(&v, p, 16);  // any alignment
-    } else {
-      uint16_t e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = 0;
-        if (c + i < nc) __builtin_memcpy(&e[i], p + 2 * i, 2);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (uint32_t)e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
-    }
-  }
-  return v;
-}
-
 // One operand of the tile: a matrix [nr][nc] (a group's part), and where the
 // tile sits in it.  KC: rows row0.. are tile rows, columns are the
 // reduction.  Otherwise rows are the reduction and columns col0.. the tile's.
-template <bool KC>
+// Rows may have any alignment: the loads are unaligned 16-byte ones, always
+// inside the matrix and without a branch around them (the compiler would
+// wait for a load where its branch ends): the row is clamped to the last
+// one and the column to the row's last eight; `put`, which runs once the
+// loads are in, moves down what a chunk at the row's end has, and puts zeros
+// outside.  SHORT: rows of fewer than eight, element by element.
+template <bool KC, bool SHORT>
 struct GenOperand {
   const char *base;
   int64_t ld, nr;
@@ -55,23 +39,66 @@ struct GenOperand {
   int32_t col0;
   u32x4 stage[4];
 
+  // row (in the step or tile) and first column of this thread's chunk q
+  __device__ __forceinline__ int chunk_row(int q) const {
+    return (q * kGenThreads + (int)threadIdx.x) / (KC ? 8 : 16);
+  }
+  __device__ __forceinline__ int chunk_col(int q, int64_t k0) const {
+    const int c = (q * kGenThreads + (int)threadIdx.x) % (KC ? 8 : 16) * 8;
+    return KC ? (int)k0 + c : col0 + c;
+  }
+
   __device__ __forceinline__ void fetch(int64_t k0) {
+    const int64_t first = KC ? row0 : k0;  // uniform: the rows' base
+    const char *rows = base + first * ld * 2;
+    const int last = (int)min((int64_t)(kGenTile - 1), nr - 1 - first);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int i = q * kGenThreads + threadIdx.x;  // chunk of the step
-      if (KC)
-        stage[q] = load8(base, ld, row0 + i / 8, (int)k0 + i % 8 * 8, nr, nc);
-      else
-        stage[q] = load8(base, ld, k0 + i / 16, col0 + i % 16 * 8, nr, nc);
+      const uint32_t row = (uint32_t)min(chunk_row(q), last) * (uint32_t)ld;
+      const int c = chunk_col(q, k0);
+      if constexpr (SHORT) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint16_t lo, hi;
+          __builtin_memcpy(&lo, rows + (row + (uint32_t)min(c + 2 * i, nc - 1)) * 2, 2);
+          __builtin_memcpy(&hi, rows + (row + (uint32_t)min(c + 2 * i + 1, nc - 1)) * 2, 2);
+          stage[q][i] = (uint32_t)lo | ((uint32_t)hi << 16);
+        }
+      } else {
+        __builtin_memcpy(&stage[q], rows + (row + (uint32_t)min(c, nc - 8)) * 2, 16);
+      }
     }
   }
-  __device__ __forceinline__ void put(char *lds) const {
+  // The chunk as it belongs in LDS: elements past the row's end and rows past
+  // the last are zeros.
+  __device__ __forceinline__ u32x4 cut(u32x4 v, int64_t row, int c) const {
+    uint64_t lo = v.x | ((uint64_t)v.y << 32), hi = v.z | ((uint64_t)v.w << 32);
+    if constexpr (SHORT) {
+      // keep the nc - c elements that exist
+      const int keep = max(0, min(8, nc - c)) * 16;
+      lo = keep >= 64 ? lo : lo & ((1ull << keep) - 1);
+      hi = keep >= 128 ? hi : (keep <= 64 ? 0 : hi & ((1ull << (keep - 64)) - 1));
+    } else if (c + 8 > nc) {
+      // loaded from nc - 8: the first 8 - nc % 8 elements are before it
+      const int sh = (8 - nc % 8) * 16;
+      lo = sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
+      hi = sh >= 64 ? 0 : hi >> sh;
+    }
+    if (row >= nr || c >= nc) lo = hi = 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  __device__ __forceinline__ void put(char *lds, int64_t k0) const {
+    // only steps and tiles at the matrix' edges need cutting
+    const bool edge = (KC ? row0 + kGenTile : k0 + kGenStep) > nr ||
+                      (KC ? k0 + kGenStep : (int64_t)col0 + kGenTile) > nc || SHORT;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = q * kGenThreads + threadIdx.x;
+      const u32x4 v = edge ? cut(stage[q], (KC ? row0 : k0) + chunk_row(q), chunk_col(q, k0))
+                           : stage[q];
       const int at = KC ? (i / 8) * 128 + ((i % 8) ^ swz<8>(i / 8)) * 16
                         : (i / 16) * 256 + ((i % 16) ^ kswz(i / 16)) * 16;
-      *(u32x4 *)(lds + at) = stage[q];
+      *(u32x4 *)(lds + at) = v;
     }
   }
   // fragment of the 32 tile rows / columns from `at`, sub-step sk
@@ -88,7 +115,7 @@ struct GenOperand {
   }
 };
 
-template <int OP, bool F16, bool OUT32>
+template <int OP, bool F16, bool OUT32, bool SHORT>
 __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a) {
   __shared__ __align__(16) char lds[2][2][kGenOperand];
   constexpr bool AKC = OP != kGroupDw, BKC = OP == kGroupProduct;
@@ -108,8 +135,8 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
     const GroupRows gr = group_rows(a, g);
     const int row0 = r / ct * kGenTile, col0 = r % ct * kGenTile;
     const int64_t welems = (int64_t)a.n * a.k;
-    GenOperand<AKC> oa;
-    GenOperand<BKC> ob;
+    GenOperand<AKC, SHORT> oa;
+    GenOperand<BKC, SHORT> ob;
     int64_t kdim;       // reduction length
     int32_t out_rows;   // rows of this group's output
     oa.base = a.a + gr.lo * a.lda * 2;
@@ -142,8 +169,8 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
     if (steps > 0) {
       oa.fetch(0);
       ob.fetch(0);
-      oa.put(lds[0][0]);
-      ob.put(lds[0][1]);
+      oa.put(lds[0][0], 0);
+      ob.put(lds[0][1], 0);
     }
     __syncthreads();
     for (int64_t s = 0; s < steps; ++s) {
@@ -167,8 +194,8 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
       }
       // the other buffer was last read in step s - 1, before its barrier
       if (s + 1 < steps) {
-        oa.put(lds[cur ^ 1][0]);
-        ob.put(lds[cur ^ 1][1]);
+        oa.put(lds[cur ^ 1][0], (s + 1) * kGenStep);
+        ob.put(lds[cur ^ 1][1], (s + 1) * kGenStep);
       }
       __syncthreads();
     }
@@ -349,8 +376,11 @@ template <int OP, bool F16, bool OUT32>
 hipError_t launch_general(const GroupArgs &a, hipStream_t st) {
   const int64_t tiles = tile_bound<OP, kGenTile>(a);
   if (tiles == 0) return hipSuccess;
-  hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32>),
-                     dim3((uint32_t)std::min(tiles, kMaxGrid)), dim3(kGenThreads), 0, st, a);
+  const dim3 grid((uint32_t)std::min(tiles, kMaxGrid)), block(kGenThreads);
+  if (a.n < 8 || a.k < 8)
+    hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
