@@ -27,6 +27,7 @@ KERNEL_KINDS = ("plan_count", "plan_rank", "dispatch", "expert_gate_up", "expert
                 "combine", "combine_copy_in", "dispatch_fp8", "stage_in_sdma", "fused")
 CCO_BF16, CCO_F16, CCO_F32 = 0, 1, 2
 CCO_SCORE_SOFTMAX, CCO_SCORE_SIGMOID = 0, 1
+CCO_GROUP_PRODUCT, CCO_GROUP_DX, CCO_GROUP_DW = 0, 1, 2
 CCO_GATE_NONE, CCO_GATE_CHANNEL, CCO_GATE_TOKEN = 0, 1, 2
 
 
@@ -99,9 +100,11 @@ SIGNATURES = [
                                              P, P, P]),
     ("cco_route", ctypes.c_int, [P, P, I32, I64, P, I32, P, P, P]),
     ("cco_route_grad", ctypes.c_int, [P, P, I32, I64, P, P, I32, P, I64, P]),
-    ("cco_group_product", ctypes.c_int, [P, I32, P, I64, P, I32, I32, P, I64, P]),
-    ("cco_group_product_dx", ctypes.c_int, [P, I32, P, I64, P, I32, I32, P, I64, P]),
-    ("cco_group_product_dw", ctypes.c_int, [P, I32, P, I64, P, I64, I32, I32, P, I32, I32, P]),
+    ("cco_group_product_workspace", U64, [I32, P, I32, I32]),
+    ("cco_group_product", ctypes.c_int, [P, I32, P, I64, P, I32, I32, P, I64, P, U64, P]),
+    ("cco_group_product_dx", ctypes.c_int, [P, I32, P, I64, P, I32, I32, P, I64, P, U64, P]),
+    ("cco_group_product_dw", ctypes.c_int, [P, I32, P, I64, P, I64, I32, I32, P, I32, I32, P, U64,
+                                            P]),
     ("cco_block_norm", ctypes.c_int, [P, P, P, I32, P, P, P]),
     ("cco_block_norm_grad_workspace", U64, [P, I32]),
     ("cco_block_norm_grad", ctypes.c_int, [P, P, P, P, P, I32, P, P, P, P, P, P, U64, P]),

@@ -1,6 +1,7 @@
 // group_common.h -- parts shared by the kernels of the products grouped by
 // expert: the groups' rows, the tile hand-out, operand fragments and the
-// layout of a tile in LDS.  Included by group.hip and group_tile.h.
+// layout of a tile in LDS.  Included by group_tile.h and
+// group_kernels.h.
 #pragma once
 
 #include "gemm_tile.h"
@@ -106,6 +107,11 @@ __device__ __forceinline__ uint16_t to_half_bits(float v) {
     return __builtin_bit_cast(uint16_t, (_Float16)v);
   else
     return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+// Two values, rounded to nearest even.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  return (uint32_t)to_half_bits<F16>(lo) | ((uint32_t)to_half_bits<F16>(hi) << 16);
 }
 template <bool F16>
 __device__ __forceinline__ float from_half_bits(uint16_t v) {

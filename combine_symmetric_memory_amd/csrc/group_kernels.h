@@ -1,9 +1,12 @@
-// group.hip -- matrix products over rows grouped by expert, with their
+// group_kernels.h -- matrix products over rows grouped by expert, with their
 // gradients (include/cco_ops.h):
 //
 //   product  y[r]  = x[r] W_g^T             rows ragged, both operands k-contiguous
 //   dx       dx[r] = dy[r] W_g              rows ragged, W_g k-major (k here: n)
 //   dw       dW_g  = sum_r dy[r]^T x[r]     reduction ragged, both k-major
+//
+// Included by group_product.hip, group_dx.hip and group_dw.hip, one direction
+// each (they compile side by side).
 //
 // Rows of whole 16 bytes take the fast kernel (group_tile.h: 256 x 256 tiles
 // fed by direct loads into LDS).
@@ -13,6 +16,8 @@
 // through two LDS buffers, the next step's operands in registers while the
 // present one is multiplied.  Every global access is checked against its
 // matrix, so any size, row distance and alignment is right.
+#pragma once
+
 #include "group_tile.h"
 
 namespace cco {
@@ -237,13 +242,16 @@ using FullTile = TileShape<OP != kGroupDw, OP == kGroupProduct, TILE, TILE, 3, T
 template <int OP>
 using WideTile = TileShape<OP != kGroupDw, OP == kGroupProduct, 128, 512, 2, 4>;
 
-template <int OP, bool F16, bool OUT32, bool ACC, int TILE>
+// SPLIT: the reduction in a.parts parts, neighbouring units of a tile, whose
+// fp32 sums go to the workspace (then OUT32).
+template <int OP, bool F16, bool OUT32, bool ACC, int TILE, bool SPLIT>
 __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_tile_kernel(
     GroupArgs a) {
   constexpr int ES = OUT32 ? 4 : 2;
   using Full = FullTile<OP, TILE>;
   using Wide = WideTile<OP>;
   constexpr bool WIDE = OP != kGroupDw && TILE == 256;
+  static_assert(!SPLIT || (OUT32 && !ACC && TILE == 128), "parts are fp32 tiles of 128");
   extern __shared__ __align__(1024) char smem[];
   // sums in accumulation registers: that form of the MFMAs draws less power
   asm volatile("" ::: "a0");
@@ -254,12 +262,15 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
   if constexpr (OP == kGroupDw)
     map.total = (int64_t)a.groups * mt * nt;
   else
-    map.init(a, (int64_t *)smem, [&](int rows) { return row_tile_units(row_tiles<TILE>(rows, ncol)); });
+    map.init(a, (int64_t *)smem,
+             [&](int rows) { return row_tile_units(row_tiles<TILE>(rows, ncol)); });
 
   GroupTile t;
   bool wide = false;
-  auto tile_at = [&](int64_t L) __attribute__((always_inline)) {
+  auto tile_at = [&](int64_t unit) __attribute__((always_inline)) {
     int g, r;
+    const int64_t L = SPLIT ? unit / a.parts : unit;
+    const int part = SPLIT ? (int)(unit - L * a.parts) : 0;
     if constexpr (OP == kGroupDw) {
       g = (int)(L / (mt * nt));
       r = (int)(L - (int64_t)g * (mt * nt));
@@ -287,7 +298,8 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
       t.a_rows = t.b_rows = 0;
       t.kdim = rows;
       t.ldc = (int64_t)a.k * ES;
-      t.c = a.c + (g * welems + (int64_t)row0 * a.k + col0) * ES;
+      t.c = SPLIT ? (char *)(a.ws + (int64_t)part * a.groups * welems) : a.c;
+      t.c += (g * welems + (int64_t)row0 * a.k + col0) * ES;
       t.c_rows = min(TILE, a.n - row0);
       t.c_cols = min(TILE, a.k - col0);
     } else {
@@ -299,17 +311,27 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
       t.a_rows = min(TILE, rows - row0);
       t.kdim = OP == kGroupProduct ? a.k : a.n;
       t.a_cols = t.a_width = 0;
-      if (OP == kGroupProduct && a.k % 2048 == 0 && a.rows <= 256 * (int64_t)a.groups)
+      if (OP == kGroupProduct && !SPLIT && a.k % 2048 == 0 && a.rows <= 256 * (int64_t)a.groups)
         t.rot = uniform((col0 / TILE + 3 * g) % (a.k / 64));
       t.b = a.b + g * welems * 2;
       if (OP == kGroupProduct) t.b += (int64_t)col0 * a.ldb * 2;
       t.b_rows = min(wide ? 512 : TILE, ncol - col0);
       t.b_cols = col0;
       t.b_width = a.k;
-      t.ldc = a.ldc * 2;
-      t.c = a.c + ((lo + row0) * a.ldc + col0) * 2;
+      const int64_t ldc = SPLIT ? ncol : a.ldc;
+      t.ldc = ldc * ES;
+      t.c = SPLIT ? (char *)(a.ws + (int64_t)part * a.rows * ncol) : a.c;
+      t.c += ((lo + row0) * ldc + col0) * ES;
       t.c_rows = t.a_rows;
       t.c_cols = t.b_rows;
+    }
+    if constexpr (SPLIT) {
+      // this part's steps (none: it leaves zeros)
+      const int64_t steps = (t.kdim + 63) / 64;
+      const int64_t kb = steps * part / a.parts, ke = steps * (part + 1) / a.parts;
+      t.a += OP == kGroupDw ? kb * 64 * t.lda : kb * 128;
+      t.b += OP == kGroupProduct ? kb * 128 : kb * 64 * t.ldb;
+      t.kdim = min(t.kdim - kb * 64, (ke - kb) * 64);
     }
     if constexpr (WIDE)
       if (wide) {
@@ -320,9 +342,10 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
   };
 
   const int xcd = blockIdx.x % kNumXcd;
-  const int64_t end = map.total * (xcd + 1) / kNumXcd;
+  const int64_t units = SPLIT ? map.total * a.parts : map.total;
+  const int64_t end = units * (xcd + 1) / kNumXcd;
   const int64_t stride = gridDim.x / kNumXcd;
-  int64_t L = map.total * xcd / kNumXcd + blockIdx.x / kNumXcd;
+  int64_t L = units * xcd / kNumXcd + blockIdx.x / kNumXcd;
   if (L >= end) return;
   tile_at(L);
   bool stored = false;
@@ -340,6 +363,14 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
   }
 }
 
+// Split reductions: products of at most kPartTiles tiles of 128 and at least
+// kSplitSteps steps of 64, into parts of at least kPartSteps.  Unsplit and
+// split: 64 tiles of 16 steps 12.4 and 16 us, 16 tiles of 22 steps 10 and 13,
+// 12 tiles of 32 steps 17 and 15, 32 tiles of 64 steps 37 and 15, 128 tiles
+// of 64 steps 39 and 32, 9 tiles of 209 steps 109 and 22, 4 tiles of 1024
+// steps 556 and 49.
+constexpr int kPartTiles = 128, kSplitSteps = 32, kPartSteps = 8, kMaxParts = 16;
+
 // Largest grid: enough workgroups that the hardware's own hand-out levels
 // uneven tiles; the kernels take further tiles in a loop.
 constexpr int64_t kMaxGrid = 4096;
@@ -353,23 +384,23 @@ int64_t tile_bound(const GroupArgs &a) {
                         : (a.rows / TILE + std::min<int64_t>(a.groups, a.rows)) * ct;
 }
 
-// Tiles of 128 where those of 256 (counted as if the rows were spread evenly
-// over the groups) would leave a third of the CUs idle: 128 tiles of 256 ran
-// 93 us and as tiles of 128 68 us (1 group, 4096 x 2048 x 4096, dw), 116 of
-// them 78 and 54 us, but 196 of them 51 and 58 us, and 256 of them 113 and
-// 141 us (8 groups, 4096 x 4096 x 4096, product).
+// Tiles of TILE as if the rows were spread evenly over the groups.
+int64_t even_tiles(GroupOp op, int tile, int64_t groups, int64_t rows, int64_t n, int64_t k) {
+  const int64_t ct = ((op == kGroupProduct ? n : k) + tile - 1) / tile;
+  if (op == kGroupDw) return groups * ct * ((n + tile - 1) / tile);
+  const int64_t g = std::max<int64_t>(1, std::min(groups, rows));
+  const int64_t avg = (rows + g - 1) / g, rem = avg % tile;
+  const bool half = tile == 256 && rem <= 128;
+  return g * (avg / tile * ct + (rem == 0 ? 0 : (half ? (ct + 1) / 2 : ct)));
+}
+
+// Tiles of 128 where those of 256 would leave a third of the CUs idle: 128
+// tiles of 256 ran 93 us and as tiles of 128 68 us (1 group, 4096 x 2048 x
+// 4096, dw), 116 of them 78 and 54 us, but 196 of them 51 and 58 us, and 256
+// of them 113 and 141 us (8 groups, 4096 x 4096 x 4096, product).
 template <int OP>
 bool small_tiles(const GroupArgs &a) {
-  int64_t tiles;
-  if (OP == kGroupDw) {
-    tiles = tile_bound<OP, 256>(a);
-  } else {
-    const int64_t ct = ((OP == kGroupProduct ? a.n : a.k) + 255) / 256;
-    const int64_t g = std::max<int64_t>(1, std::min<int64_t>(a.groups, a.rows));
-    const int64_t avg = (a.rows + g - 1) / g, rem = avg % 256;
-    tiles = g * (avg / 256 * ct + (rem == 0 ? 0 : (rem <= 128 ? (ct + 1) / 2 : ct)));
-  }
-  return 3 * tiles < 2 * kNumCus;
+  return 3 * even_tiles((GroupOp)OP, 256, a.groups, a.rows, a.n, a.k) < 2 * kNumCus;
 }
 
 template <int OP, bool F16, bool OUT32>
@@ -393,15 +424,76 @@ hipError_t launch_tiles(const GroupArgs &a, hipStream_t st) {
   const dim3 g((uint32_t)grid), b(kGemmWaves * kWave);
   constexpr int lds = FullTile<OP, TILE>::LDS_BYTES;
   if (OP == kGroupDw && a.accumulate)
-    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, OP == kGroupDw, TILE>), g, b, lds, st, a);
+    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, OP == kGroupDw, TILE, false>), g, b, lds,
+                       st, a);
   else
-    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, false, TILE>), g, b, lds, st, a);
+    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, false, TILE, false>), g, b, lds, st, a);
+  return hipGetLastError();
+}
+
+// C = the parts' sums, in order (dw: added to what is there).  Block y is a
+// group; its elements of a part are contiguous, rows of C columns.
+template <int OP, bool F16, bool OUT32>
+__global__ __launch_bounds__(256) void group_parts_kernel(GroupArgs a) {
+  const int g = blockIdx.y;
+  const int64_t cols = OP == kGroupProduct ? a.n : a.k;
+  int64_t lo = (int64_t)g * a.n, n = a.n, part = (int64_t)a.groups * a.n * cols;
+  if (OP != kGroupDw) {
+    const GroupRows gr = group_rows(a, g);
+    lo = gr.lo;
+    n = gr.n;
+    part = (int64_t)a.rows * cols;
+  }
+  const float *ws = a.ws + lo * cols;
+  // four elements a thread (columns are a multiple of 8)
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n * cols;
+       i += (int64_t)gridDim.x * 1024) {
+    f32x4 s = *(const f32x4 *)(ws + i);
+    for (int p = 1; p < a.parts; ++p) s += *(const f32x4 *)(ws + p * part + i);
+    const int64_t row = lo + i / cols, col = i % cols;
+    char *c = a.c + (row * (OP == kGroupDw ? cols : a.ldc) + col) * (OUT32 ? 4 : 2);
+    if constexpr (OUT32) {
+      if (a.accumulate) s += *(const f32x4 *)c;
+      *(f32x4 *)c = s;
+    } else {
+      u32x2 d;
+      if (a.accumulate) {
+        d = *(const u32x2 *)c;
+        const uint32_t d0 = d.x, d1 = d.y;
+        s[0] += from_half_bits<F16>((uint16_t)d0);
+        s[1] += from_half_bits<F16>((uint16_t)(d0 >> 16));
+        s[2] += from_half_bits<F16>((uint16_t)d1);
+        s[3] += from_half_bits<F16>((uint16_t)(d1 >> 16));
+      }
+      d.x = pack_half<F16>(s[0], s[1]);
+      d.y = pack_half<F16>(s[2], s[3]);
+      *(u32x2 *)c = d;
+    }
+  }
+}
+
+template <int OP, bool F16, bool OUT32>
+hipError_t launch_split(const GroupArgs &a, hipStream_t st) {
+  const int64_t tiles = tile_bound<OP, 128>(a);
+  if (tiles == 0) return hipSuccess;
+  const int64_t units = tiles * a.parts;
+  const int64_t grid = std::min((units + kNumXcd - 1) / kNumXcd * kNumXcd, kMaxGrid);
+  hipLaunchKernelGGL((group_tile_kernel<OP, F16, true, false, 128, true>), dim3((uint32_t)grid),
+                     dim3(kGemmWaves * kWave), (FullTile<OP, 128>::LDS_BYTES), st, a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int64_t cols = OP == kGroupProduct ? a.n : a.k;
+  const int64_t elems = OP == kGroupDw ? a.n * cols : (a.rows + a.groups - 1) / a.groups * cols;
+  const int64_t gx = std::min<int64_t>(std::max<int64_t>(1, (elems + 1023) / 1024), 1024);
+  hipLaunchKernelGGL((group_parts_kernel<OP, F16, OUT32>), dim3((uint32_t)gx, a.groups), dim3(256),
+                     0, st, a);
   return hipGetLastError();
 }
 
 template <int OP, bool F16, bool OUT32>
 hipError_t launch_either(bool aligned, const GroupArgs &a, hipStream_t st) {
   if (!aligned) return launch_general<OP, F16, OUT32>(a, st);
+  if (a.parts > 1) return launch_split<OP, F16, OUT32>(a, st);
   return small_tiles<OP>(a) ? launch_tiles<OP, F16, OUT32, 128>(a, st)
                             : launch_tiles<OP, F16, OUT32, 256>(a, st);
 }
@@ -417,14 +509,4 @@ hipError_t launch_op(bool f16, bool out_f32, bool aligned, const GroupArgs &a, h
 }
 
 }  // namespace
-
-hipError_t launch_group(GroupOp op, bool f16, bool out_f32, bool aligned, const GroupArgs &a,
-                        hipStream_t st) {
-  switch (op) {
-    case kGroupProduct: return launch_op<kGroupProduct>(f16, out_f32, aligned, a, st);
-    case kGroupDx: return launch_op<kGroupDx>(f16, out_f32, aligned, a, st);
-    default: return launch_op<kGroupDw>(f16, out_f32, aligned, a, st);
-  }
-}
-
 }  // namespace cco

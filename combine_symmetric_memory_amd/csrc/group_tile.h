@@ -1,5 +1,5 @@
 // group_tile.h -- one tile of the products grouped by expert for rows of
-// whole 16 bytes: the fast kernel's work, included by group.hip.
+// whole 16 bytes: the fast kernel's work, included by group_kernels.h.
 //
 // Four wavefronts, one per SIMD, each with 128 x 128 of the output as 4 x 4
 // blocks of 32x32x16 MFMAs whose sums sit in the 256 accumulation registers.
@@ -119,7 +119,8 @@ struct TileLoads {
   }
   // load q of this wavefront's share, into the slot at `lds`
   __device__ __forceinline__ void issue(const Step &s, int q, char *lds, int wave) const {
-    buffer_load_lds_16(s.r, s.v + (uint32_t)q * step_ld, s.soff, lds + (q * kGemmWaves + wave) * 1024);
+    buffer_load_lds_16(s.r, s.v + (uint32_t)q * step_ld, s.soff,
+                       lds + (q * kGemmWaves + wave) * 1024);
   }
 };
 
@@ -360,7 +361,9 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
     else
       wait_vmcnt<BEHIND>();
     stage_barrier();
-    static_for<NRD>([&](auto r_c) __attribute__((always_inline)) { read(I0{}, I0{}, r_c, 0u, 0u); });
+    static_for<NRD>([&](auto r_c) __attribute__((always_inline)) {
+      read(I0{}, I0{}, r_c, 0u, 0u);
+    });
     // Step kt: A slot AS = kt % 2, B slot bs = kt % RB.  The batch issued
     // after its barrier: A of kt + 2 and B of kt + RB, into the same slots.
     auto step = [&](auto as_c, int kt, int bs) __attribute__((always_inline)) {
@@ -454,8 +457,8 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
           u32x4 o[ITS];
 #pragma unroll
           for (int it = 0; it < ITS; ++it)
-            o[it] = __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
-                                                          (int)soff, 0);
+            o[it] = __builtin_amdgcn_raw_buffer_load_b128(
+                rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), (int)soff, 0);
 #pragma unroll
           for (int it = 0; it < ITS; ++it)
             w[it] = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, w[it]) +
@@ -476,10 +479,10 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
           const f32x4 f = __builtin_bit_cast(f32x4, w[it]);
           const uint32_t o0 = o[it].x, o1 = o[it].y;
           u32x2 d;
-          d.x = (uint32_t)to_half_bits<F16>(f[0] + from_half_bits<F16>((uint16_t)o0)) |
-                ((uint32_t)to_half_bits<F16>(f[1] + from_half_bits<F16>((uint16_t)(o0 >> 16))) << 16);
-          d.y = (uint32_t)to_half_bits<F16>(f[2] + from_half_bits<F16>((uint16_t)o1)) |
-                ((uint32_t)to_half_bits<F16>(f[3] + from_half_bits<F16>((uint16_t)(o1 >> 16))) << 16);
+          d.x = pack_half<F16>(f[0] + from_half_bits<F16>((uint16_t)o0),
+                               f[1] + from_half_bits<F16>((uint16_t)(o0 >> 16)));
+          d.y = pack_half<F16>(f[2] + from_half_bits<F16>((uint16_t)o1),
+                               f[3] + from_half_bits<F16>((uint16_t)(o1 >> 16)));
           __builtin_amdgcn_raw_buffer_store_b64(d, rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
                                                 (int)soff, 0);
         }
@@ -495,8 +498,7 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
           uint32_t d[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            d[e] = (uint32_t)to_half_bits<F16>(acc[i][j][8 * q + 2 * e]) |
-                   ((uint32_t)to_half_bits<F16>(acc[i][j][8 * q + 2 * e + 1]) << 16);
+            d[e] = pack_half<F16>(acc[i][j][8 * q + 2 * e], acc[i][j][8 * q + 2 * e + 1]);
           // lanes l and l ^ 32 trade halves: eight columns a lane
           swap_halves(d[0], d[2]);
           swap_halves(d[1], d[3]);
@@ -561,7 +563,9 @@ __device__ __forceinline__ RowTiles row_tiles(int rows, int ncol) {
   t.bands = max(1, (t.full + kBand - 1) / kBand);
   return t;
 }
-__device__ __forceinline__ int row_tile_units(const RowTiles &t) { return t.full * t.ntl + t.nwide; }
+__device__ __forceinline__ int row_tile_units(const RowTiles &t) {
+  return t.full * t.ntl + t.nwide;
+}
 
 // Unit r: its first row, first column, and whether it is a wide tile.
 template <int TILE>

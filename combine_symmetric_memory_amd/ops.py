@@ -179,7 +179,8 @@ def route_grad(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor, *,
     else:
         ldo = _rows(out, dev, "out", E, T, logits.dtype)
     check(lib.cco_route_grad(ctypes.byref(d), logits.data_ptr(), code, ld, idx.data_ptr(),
-                             dw.data_ptr(), T, out.data_ptr(), ldo, _raw_stream(dev.index)), "cco_route_grad")
+                             dw.data_ptr(), T, out.data_ptr(), ldo, _raw_stream(dev.index)),
+          "cco_route_grad")
     return out
 
 
@@ -194,6 +195,12 @@ def _groups(first, count, rows, dev):
     _same(first, dev, "first", (n,), torch.int32)
     _same(count, dev, "count", (n,), torch.int32)
     return _capi.cco_groups(n, rows, first.data_ptr(), count.data_ptr())
+
+
+def _workspace(op: int, g, n: int, k: int, dev):
+    """(tensor or None, bytes) with which a product splits its reduction."""
+    nbytes = lib.cco_group_product_workspace(op, ctypes.byref(g), n, k)
+    return (torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None), nbytes
 
 
 def group_product(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
@@ -216,8 +223,10 @@ def group_product(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, w: 
     if out is None:
         out = torch.empty((rows, n), dtype=x.dtype, device=dev)
     ldy = _rows(out, dev, "out", n, rows, x.dtype)
+    ws, nbytes = _workspace(_capi.CCO_GROUP_PRODUCT, g, n, k, dev)
     check(lib.cco_group_product(ctypes.byref(g), code, x.data_ptr(), ldx, w.data_ptr(), n, k,
-                                out.data_ptr(), ldy, _raw_stream(dev.index)), "cco_group_product")
+                                out.data_ptr(), ldy, _p(ws), nbytes, _raw_stream(dev.index)),
+          "cco_group_product")
     return out
 
 
@@ -240,8 +249,10 @@ def group_product_dx(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     if out is None:
         out = torch.empty((rows, k), dtype=dy.dtype, device=dev)
     lddx = _rows(out, dev, "out", k, rows, dy.dtype)
+    ws, nbytes = _workspace(_capi.CCO_GROUP_DX, g, n, k, dev)
     check(lib.cco_group_product_dx(ctypes.byref(g), code, dy.data_ptr(), lddy, w.data_ptr(),
-                                   n, k, out.data_ptr(), lddx, _raw_stream(dev.index)),
+                                   n, k, out.data_ptr(), lddx, _p(ws), nbytes,
+                                   _raw_stream(dev.index)),
           "cco_group_product_dx")
     return out
 
@@ -267,9 +278,11 @@ def group_product_dw(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     if out is None:
         out = torch.empty((g.groups, n, k), dtype=dy.dtype, device=dev)
     _same(out, dev, "out", (g.groups, n, k))
+    ws, nbytes = _workspace(_capi.CCO_GROUP_DW, g, n, k, dev)
     check(lib.cco_group_product_dw(ctypes.byref(g), code, dy.data_ptr(), lddy, x.data_ptr(),
                                    ldx, n, k, out.data_ptr(), _dtype(out, "out"),
-                                   int(bool(accumulate)), _raw_stream(dev.index)), "cco_group_product_dw")
+                                   int(bool(accumulate)), _p(ws), nbytes,
+                                   _raw_stream(dev.index)), "cco_group_product_dw")
     return out
 
 

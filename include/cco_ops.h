@@ -99,20 +99,34 @@ typedef struct {
   const int32_t *count; /* [groups] */
 } cco_groups;
 
+/* Which product (for the workspace query). */
+typedef enum { CCO_GROUP_PRODUCT = 0, CCO_GROUP_DX = 1, CCO_GROUP_DW = 2 } cco_group_op;
+
+/* Bytes of workspace with which a product of these sizes splits its
+ * reduction over workgroups; 0: it never does (or invalid sizes).  Products
+ * with few output tiles and long reductions are split, so that they occupy
+ * the GPU: the parts' fp32 sums go to the workspace and a second kernel adds
+ * them in order.  Without workspace the same products run unsplit, slower
+ * (and may differ from the split ones by the order of their sums). */
+uint64_t cco_group_product_workspace(int32_t op, const cco_groups *g, int32_t n, int32_t k);
+
 /* y[r][n] = sum_k x[r][k] * w[g][n][k] for the rows r of every group g.
  *   dtype  CCO_BF16 or CCO_F16, for x, w and y; sums in fp32
  *   x      [rows][k], row distance ldx;  w  [groups][n][k], dense
  *   y      [rows][n], row distance ldy
  * n, k and the row distances lie in [1, 2^21).
  * Rows of whole 16 bytes (n, k and the distances multiples of 8, pointers
- * 16-byte aligned) take the fast kernel, others a general one. */
+ * 16-byte aligned) take the fast kernel, others a general one.
+ *   workspace  NULL, or device memory of at least the size above, 16-byte
+ *              aligned, in use until the call's kernels have run */
 int cco_group_product(const cco_groups *g, int32_t dtype, const void *x, int64_t ldx,
-                      const void *w, int32_t n, int32_t k, void *y, int64_t ldy, void *stream);
+                      const void *w, int32_t n, int32_t k, void *y, int64_t ldy, void *workspace,
+                      uint64_t workspace_bytes, void *stream);
 
 /* Gradient to the rows: dx[r][k] = sum_n dy[r][n] * w[g][n][k]. */
 int cco_group_product_dx(const cco_groups *g, int32_t dtype, const void *dy, int64_t lddy,
                          const void *w, int32_t n, int32_t k, void *dx, int64_t lddx,
-                         void *stream);
+                         void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Gradient to the weights: dw[g][n][k] = sum over the rows r of group g of
  * dy[r][n] * x[r][k], a group without rows giving zeros; with `accumulate`
@@ -121,7 +135,8 @@ int cco_group_product_dx(const cco_groups *g, int32_t dtype, const void *dy, int
  *              CCO_F32 */
 int cco_group_product_dw(const cco_groups *g, int32_t dtype, const void *dy, int64_t lddy,
                          const void *x, int64_t ldx, int32_t n, int32_t k, void *dw,
-                         int32_t out_dtype, int32_t accumulate, void *stream);
+                         int32_t out_dtype, int32_t accumulate, void *workspace,
+                         uint64_t workspace_bytes, void *stream);
 
 /* --------------------------------------------- norms around a block ---- */
 

@@ -132,7 +132,8 @@ def _check(cco, T, H, dtype, wdtype=F32, post=True, gate="none", pre=True, y=Tru
             ref.assert_within(got[3], want["gate"], (2 * E + chain) * (abs(scale) * z * ad).sum(0),
                               "dgate")
         elif gate == "token":
-            ref.assert_within(got[3], want["token_gate"], 2 * E * (abs(scale) * z * ad).sum(1), "dgate")
+            ref.assert_within(got[3], want["token_gate"], 2 * E * (abs(scale) * z * ad).sum(1),
+                              "dgate")
     if pre:
         chain = (T / 64 + 40) * ref.U
         ref.assert_within(got[4], want["pre"],

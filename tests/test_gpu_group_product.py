@@ -274,3 +274,37 @@ def test_offsets_past_32_bits(cco):
     cco.group_product_dx(f, c, dy, w, out=dx)
     v, s = ref.product(dy[-40:].cpu(), w[1].cpu())
     ref.assert_within(dx[-40:], v, ref.product_bound(v, s, n, BF), "dx behind 4 GiB")
+
+
+@pytest.mark.parametrize("counts,n,k", [([40], 128, 2048), ([3, 0, 17], 72, 4104),
+                                        ([1], 2056, 64), ([2100], 64, 72), ([9000, 0, 5], 40, 136)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_split_reductions(cco, counts, n, k, dtype):
+    # few tiles and long reductions in one of the three directions
+    first, count = _packed(counts)
+    _check_all(cco, first, count, sum(counts), n, k, dtype, pads=(8, 8), seed=n)
+
+
+def test_a_split_reduction_needs_its_workspace_and_keeps_other_rows(cco):
+    import ctypes
+    from combine_symmetric_memory_amd import _capi
+    n, k, rows = 136, 4096, 90
+    x, w = _rand((rows, k), BF, 1), _rand((2, n, k), BF, 2)
+    f, c = _i32([70, 0]), _i32([15, 50])
+    g = _capi.cco_groups(2, rows, f.data_ptr(), c.data_ptr())
+    nbytes = _capi.lib.cco_group_product_workspace(0, ctypes.byref(g), n, k)
+    assert nbytes > 0
+    ws = torch.full((nbytes + 64,), 7, dtype=torch.uint8, device="cuda")
+    outs = []
+    for p, size in ((None, 0), (ws.data_ptr(), nbytes)):
+        out = torch.full((rows, n), 3.0, dtype=BF, device="cuda")
+        assert _capi.lib.cco_group_product(ctypes.byref(g), 0, x.data_ptr(), k, w.data_ptr(), n, k,
+                                           out.data_ptr(), n, p, size,
+                                           torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert bool((out[50:70] == 3).all()) and bool((out[85:] == 3).all())
+        for lo, hi, e in ((70, 85, 0), (0, 50, 1)):
+            v, s = ref.product(x[lo:hi].cpu(), w[e].cpu().t())
+            ref.assert_within(out[lo:hi], v, ref.product_bound(v, s, k, BF), "group %d" % e)
+        outs.append(out)
+    assert bool((ws[nbytes:] == 7).all())

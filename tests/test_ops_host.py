@@ -57,9 +57,9 @@ def _groups(capi, groups=4, rows=16, first=P, count=P):
 def test_groups(capi, kw):
     g = _groups(capi, **kw)
     L = capi.lib
-    assert L.cco_group_product(g, 0, P, 8, P, 8, 8, P, 8, None) == -1
-    assert L.cco_group_product_dx(g, 0, P, 8, P, 8, 8, P, 8, None) == -1
-    assert L.cco_group_product_dw(g, 0, P, 8, P, 8, 8, 8, P, 0, 0, None) == -1
+    assert L.cco_group_product(g, 0, P, 8, P, 8, 8, P, 8, None, 0, None) == -1
+    assert L.cco_group_product_dx(g, 0, P, 8, P, 8, 8, P, 8, None, 0, None) == -1
+    assert L.cco_group_product_dw(g, 0, P, 8, P, 8, 8, 8, P, 0, 0, None, 0, None) == -1
 
 
 def test_group_product_arguments(capi):
@@ -70,19 +70,40 @@ def test_group_product_arguments(capi):
               (0, P, 8, P, 8, 8, None, 8), (0, P, 8, P, 8, 8, P, 7), (0, P + 1, 8, P, 8, 8, P, 8),
               (0, P, 8, P + 1, 8, 8, P, 8), (0, P, 8, P, 8, 8, P + 1, 8), (9, P, 8, P, 8, 8, P, 8),
               (0, P, big, P, 8, 8, P, 8), (0, P, 8, P, big, 8, P, big)):
-        assert L.cco_group_product(g, *a, None) == -1, a
-        assert L.cco_group_product_dx(g, *a, None) == -1, a
+        assert L.cco_group_product(g, *a, None, 0, None) == -1, a
+        assert L.cco_group_product_dx(g, *a, None, 0, None) == -1, a
     for a in ((2, P, 8, P, 8, 8, 8, P, 2, 0), (0, P, 8, P, 8, 8, 8, P, 1, 0),
               (0, P, 7, P, 8, 8, 8, P, 0, 0), (0, P, 8, P, 7, 8, 8, P, 0, 0),
               (0, P, 8, P, 8, 8, 8, None, 0, 0), (0, P, 8, P, 8, 8, 8, P + 2, 2, 0),
               (0, None, 8, P, 8, 8, 8, P, 0, 0)):
-        assert L.cco_group_product_dw(g, *a, None) == -1, a
-    assert L.cco_group_product(None, 0, P, 8, P, 8, 8, P, 8, None) == -1
+        assert L.cco_group_product_dw(g, *a, None, 0, None) == -1, a
+    assert L.cco_group_product(None, 0, P, 8, P, 8, 8, P, 8, None, 0, None) == -1
     # no rows: nothing to do, and nothing launched
     none = _groups(capi, rows=0)
-    assert L.cco_group_product(none, 0, None, 8, P, 8, 8, None, 8, None) == 0
-    assert L.cco_group_product_dx(none, 0, None, 8, P, 8, 8, None, 8, None) == 0
-    assert L.cco_group_product_dw(none, 0, None, 8, None, 8, 8, 8, P, 0, 1, None) == 0
+    assert L.cco_group_product(none, 0, None, 8, P, 8, 8, None, 8, None, 0, None) == 0
+    assert L.cco_group_product_dx(none, 0, None, 8, P, 8, 8, None, 8, None, 0, None) == 0
+    assert L.cco_group_product_dw(none, 0, None, 8, None, 8, 8, 8, P, 0, 1, None, 0, None) == 0
+
+
+def test_group_workspace(capi):
+    L = capi.lib
+    W = L.cco_group_product_workspace
+    # few tiles and a long reduction: parts of the fp32 result
+    one = _groups(capi, groups=1, rows=64)
+    n = W(capi.CCO_GROUP_PRODUCT, one, 256, 8192)
+    assert n > 0 and n % (64 * 256 * 4) == 0 and n // (64 * 256 * 4) >= 2
+    assert W(capi.CCO_GROUP_DX, one, 8192, 256) > 0
+    assert W(capi.CCO_GROUP_DW, _groups(capi, groups=1, rows=8192), 64, 256) > 0
+    # none where nothing is split: many tiles, short reductions, rows of
+    # other than whole 16 bytes, no rows, bad arguments
+    assert W(capi.CCO_GROUP_PRODUCT, _groups(capi, groups=64, rows=65536), 4096, 8192) == 0
+    assert W(capi.CCO_GROUP_PRODUCT, one, 256, 64) == 0
+    assert W(capi.CCO_GROUP_PRODUCT, one, 257, 8192) == 0
+    assert W(capi.CCO_GROUP_PRODUCT, _groups(capi, rows=0), 256, 8192) == 0
+    assert W(3, one, 256, 8192) == 0 and W(0, None, 256, 8192) == 0
+    # too small or misaligned
+    for ws, size in ((P, n - 1), (P + 8, n)):
+        assert L.cco_group_product(one, 0, P, 8192, P, 256, 8192, P, 256, ws, size, None) == -1
 
 
 def _norm(capi, H=64, dtype=0, wdtype=2, kind=0, eps=1e-6, post=None, gate=None, pre=P):
