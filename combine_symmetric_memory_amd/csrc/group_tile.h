@@ -22,6 +22,15 @@
 //   k-major operand       one descriptor per step, as long as the rows left
 // Fragments of a k-major operand come from LDS by transposing reads.
 //
+// Measured: 8 groups of 1024 rows by 14336 x 4096, product and dx 1.22
+// PFLOP/s, one group of 65536 rows by 4096 x 4096, dw 1.28 (bound by the
+// matrix cores' clock under load and the operands' way through LDS, no bank
+// conflicts); 256 groups of 8 rows by 7168 x 2048, product 5.9 TB/s of
+// weights.  A tile's results and first loads cost about 17000 cycles of the
+// 3400 a step takes, so reductions of few steps stay below (16 steps: 1.0
+// PFLOP/s, with fp32 results 0.87: loads and stores complete in one order,
+// and the third step waits for the last tile's stores).
+//
 // A step is four MFMA sub-steps on two fragment buffers in turn: while one
 // is multiplied the other is read, and the loads of a later step are spread
 // between the MFMAs.  One barrier per step, in the last sub-step: after it
@@ -414,6 +423,11 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
     // staged row r lies at c ^ (r % chunks).
     // Rows and columns that do not exist are cut off by the buffer's range
     // (columns by the offset's top bit): every store is issued.
+    // The stores' whole offset is in the vector register: with a scalar
+    // register added, the compiler takes the stored registers to be free at
+    // once, and an instruction right behind a 16-byte store that writes them
+    // was seen to change what lanes 12..15 of 16 store.  Without one it keeps
+    // the distance.
     constexpr int ES = OUT32 ? 4 : 2;
     typedef __attribute__((address_space(3))) u32x4 lds_u32x4_rw;
     constexpr int SROW = Shape::STAGE_ROW, CH = SROW / 16;  // bytes and chunks of a row
@@ -443,9 +457,8 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
         }
       });
       const int col = wn * FN * 32 + pass * FN * 16 + schunk * 4;
-      const uint32_t soff = (uint32_t)((wm + i * WM) * 32) * ldc;
-      const uint32_t v0 =
-          ((uint32_t)srow * ldc + (uint32_t)col * ES) | (col < t.c_cols ? 0u : 0x80000000u);
+      const uint32_t v0 = ((uint32_t)((wm + i * WM) * 32 + srow) * ldc + (uint32_t)col * ES) |
+                          (col < t.c_cols ? 0u : 0x80000000u);
       u32x4 w[ITS];
 #pragma unroll
       for (int it = 0; it < ITS; ++it) {
@@ -458,7 +471,7 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
 #pragma unroll
           for (int it = 0; it < ITS; ++it)
             o[it] = __builtin_amdgcn_raw_buffer_load_b128(
-                rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), (int)soff, 0);
+                rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), 0, 0);
 #pragma unroll
           for (int it = 0; it < ITS; ++it)
             w[it] = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, w[it]) +
@@ -466,14 +479,14 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
         }
 #pragma unroll
         for (int it = 0; it < ITS; ++it)
-          __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
-                                                 (int)soff, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), 0,
+                                                 0);
       } else {
         u32x2 o[ITS];
 #pragma unroll
         for (int it = 0; it < ITS; ++it)
-          o[it] = __builtin_amdgcn_raw_buffer_load_b64(rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
-                                                       (int)soff, 0);
+          o[it] = __builtin_amdgcn_raw_buffer_load_b64(rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), 0,
+                                                 0);
 #pragma unroll
         for (int it = 0; it < ITS; ++it) {
           const f32x4 f = __builtin_bit_cast(f32x4, w[it]);
@@ -483,8 +496,8 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
                                f[1] + from_half_bits<F16>((uint16_t)(o0 >> 16)));
           d.y = pack_half<F16>(f[2] + from_half_bits<F16>((uint16_t)o1),
                                f[3] + from_half_bits<F16>((uint16_t)(o1 >> 16)));
-          __builtin_amdgcn_raw_buffer_store_b64(d, rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
-                                                (int)soff, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(d, rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), 0,
+                                                 0);
         }
       }
     };
@@ -508,9 +521,8 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
         }
       });
       const int col = wn * FN * 32 + schunk * 8;
-      const uint32_t soff = (uint32_t)((wm + i * WM) * 32) * ldc;
-      const uint32_t v0 =
-          ((uint32_t)srow * ldc + (uint32_t)col * 2) | (col < t.c_cols ? 0u : 0x80000000u);
+      const uint32_t v0 = ((uint32_t)((wm + i * WM) * 32 + srow) * ldc + (uint32_t)col * 2) |
+                          (col < t.c_cols ? 0u : 0x80000000u);
       u32x4 w[ITS];
 #pragma unroll
       for (int it = 0; it < ITS; ++it) {
@@ -519,8 +531,8 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
       }
 #pragma unroll
       for (int it = 0; it < ITS; ++it)
-        __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * RPS) * ldc),
-                                               (int)soff, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(w[it], rc, (int)(v0 + (uint32_t)(it * RPS) * ldc), 0,
+                                                 0);
     };
     if constexpr (OUT32 || ACC)
       static_for<NACT>([&](auto i_c) __attribute__((always_inline)) {

@@ -78,7 +78,7 @@ int cco_route(const cco_route_desc *d, const void *logits, int32_t dtype, int64_
  * logits' type, row distance lddl.  Of `d` the num_experts, topk, score,
  * renorm and scale count.  The ids may be any: one outside [0, E) takes no
  * part, one that occurs twice counts twice (in the renormalising sum too).
- * dw device fp32 [T][K]. */
+ * dw device fp32 [T][K].  dlogits may be logits (in place, lddl = ld). */
 int cco_route_grad(const cco_route_desc *d, const void *logits, int32_t dtype, int64_t ld,
                    const int32_t *idx, const float *dw, int32_t T, void *dlogits, int64_t lddl,
                    void *stream);

@@ -367,3 +367,25 @@ def test_fused_combine_with_dropped_pairs_and_many_choices(cco):
         want = cco.block_norm(c.x, y, pre=pre)
         out, u, _ = cco.combine_norm(moe, c.x, c.w, pre=pre)
         assert torch.equal(out, want[0]) and torch.equal(u, want[1])
+
+
+def test_rows_past_32_bits(cco):
+    # more than 2^31 elements: the last rows lie behind 4 GiB
+    T, H = 300_000, 7168
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    y = torch.zeros((T, H), dtype=BF, device="cuda")
+    d = _inputs(3, H, BF, F32, True, "channel", True)
+    x[-3:], y[-3:] = d["x"].cuda(), d["y"].cuda()
+    kw = dict(_kw(d), scale=0.7, eps=EPS)
+    out, u = cco.block_norm(x, y, **kw)
+    want = cco.block_norm(x[-3:].contiguous(), y[-3:].contiguous(), **kw)
+    assert torch.equal(out[-3:], want[0]) and torch.equal(u[-3:], want[1])
+    assert not out[:-3].any()
+    dout, du = out.zero_(), u.zero_()
+    dout[-3:], du[-3:] = d["dout"].cuda(), d["du"].cuda()
+    got = cco.block_norm_grad(x, y, dout, du, dx=dout, dy=du, **kw)
+    wg = cco.block_norm_grad(d["x"].cuda(), d["y"].cuda(), d["dout"].cuda(), d["du"].cuda(), **kw)
+    for i in (0, 1):
+        assert torch.equal(got[i][-3:], wg[i]) and not got[i][:-3].any()
+    for i in (2, 3, 4):  # three rows' terms, at most in another order
+        assert bool(((got[i] - wg[i]).abs() <= 8 * ref.U * 60 * (1 + wg[i].abs())).all())

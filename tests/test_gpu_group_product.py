@@ -308,3 +308,62 @@ def test_a_split_reduction_needs_its_workspace_and_keeps_other_rows(cco):
             ref.assert_within(out[lo:hi], v, ref.product_bound(v, s, k, BF), "group %d" % e)
         outs.append(out)
     assert bool((ws[nbytes:] == 7).all())
+
+
+def test_smallest_numbers(cco):
+    # subnormal operands, products and results count like any others
+    f, c = _i32([0]), _i32([33])
+    for dtype, tiny in ((HF, 2.0 ** -22), (BF, 2.0 ** -130)):
+        g = torch.Generator().manual_seed(1)
+        x = (torch.randint(-3, 4, (33, 72), generator=g) * tiny).to(dtype)
+        w = torch.randint(-2, 3, (1, 40, 72), generator=g).to(dtype)
+        for k in (72, 65):
+            y = cco.group_product(f, c, x[:, :k].contiguous().cuda(),
+                                  w[:, :, :k].contiguous().cuda())
+            want = x[:, :k].double() @ w[0, :, :k].double().t()
+            # sums of few integers times tiny: exact before the one rounding
+            bound = ref.half_step(dtype) * want.abs() + ref.smallest(dtype)
+            ref.assert_within(y, want, bound, "%s k=%d" % (dtype, k))
+
+
+@pytest.mark.parametrize("rows,n,k,groups", [(80, 64, 7168, 2), (4096, 64, 512, 1),
+                                             (300, 264, 520, 3), (2000, 2048, 2048, 7),
+                                             (40, 4096, 128, 2)])
+def test_repeats_are_equal_bit_for_bit(cco, rows, n, k, groups):
+    # every tile form, split and not, into poisoned outputs: a store that
+    # takes a register too late shows as a few wrong elements now and then
+    counts = [rows // groups] * groups
+    first, count = _packed(counts)
+    f, c = _i32(first), _i32(count)
+    rows = sum(counts)
+    x, dy, w = _rand((rows, k), BF, 1), _rand((rows, n), BF, 2), _rand((groups, n, k), BF, 3)
+    old = _rand((groups, n, k), F32, 4)
+    outs = [torch.empty((rows, n), dtype=BF, device="cuda"),
+            torch.empty((rows, k), dtype=BF, device="cuda"),
+            torch.empty((groups, n, k), dtype=BF, device="cuda"),
+            torch.empty((groups, n, k), dtype=F32, device="cuda"),
+            torch.empty((groups, n, k), dtype=F32, device="cuda"),
+            torch.empty((groups, n, k), dtype=BF, device="cuda")]
+
+    def run():
+        for o in outs[:4]:
+            o.fill_(float("nan"))
+        outs[4].copy_(old)
+        outs[5].copy_(old)
+        cco.group_product(f, c, x, w, out=outs[0])
+        cco.group_product_dx(f, c, dy, w, out=outs[1])
+        cco.group_product_dw(f, c, dy, x, out=outs[2])
+        cco.group_product_dw(f, c, dy, x, out=outs[3])
+        cco.group_product_dw(f, c, dy, x, out=outs[4], accumulate=True)
+        cco.group_product_dw(f, c, dy, x, out=outs[5], accumulate=True)
+
+    run()
+    want = [o.clone() for o in outs]
+    assert torch.allclose(want[3] + old, want[4], atol=1e-4, rtol=1e-5)
+    assert bool((want[3].to(BF) == want[2]).all())
+    differ = torch.zeros(len(outs), dtype=torch.int64, device="cuda")
+    for _ in range(50):
+        run()
+        for i, o in enumerate(outs):
+            differ[i] += (o != want[i]).sum()
+    assert differ.tolist() == [0] * len(outs)

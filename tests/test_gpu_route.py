@@ -241,3 +241,20 @@ def test_no_tokens(cco):
     idx, w = cco.route(torch.empty((0, 8), device="cuda"), 2)
     assert idx.shape == (0, 2) and w.shape == (0, 2)
     assert cco.route_grad(torch.empty((0, 8), device="cuda"), idx, w).shape == (0, 8)
+
+
+def test_tokens_past_32_bits(cco):
+    T, E = 8_400_000, 256
+    logits = torch.zeros((T, E), dtype=BF, device="cuda")
+    g = torch.Generator().manual_seed(6)
+    tail = torch.randn((5, E), generator=g).to(BF)
+    logits[-5:] = tail.cuda()
+    idx, w = cco.route(logits, 4, score="sigmoid", renorm=True)
+    i2, w2 = cco.route(tail.cuda(), 4, score="sigmoid", renorm=True)
+    assert torch.equal(idx[-5:], i2) and torch.equal(w[-5:], w2)
+    assert idx[0].tolist() == [0, 1, 2, 3]
+    dw = torch.ones((T, 4), device="cuda")
+    dw[-5:, 1] = -2
+    got = cco.route_grad(logits, idx, dw, score="sigmoid", renorm=True, out=logits)
+    want = cco.route_grad(tail.cuda(), i2, dw[-5:].contiguous(), score="sigmoid", renorm=True)
+    assert torch.equal(got[-5:], want) and not got[:-5].any()

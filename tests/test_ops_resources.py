@@ -63,3 +63,14 @@ def test_tile_loops_stay_in_registers(asm, src):
             seen += 1
             assert "scratch_" not in b and "v_accvgpr" not in b, fn
     assert seen >= 10
+
+
+@pytest.mark.parametrize("src", FILES)
+def test_wide_buffer_stores_have_no_scalar_offset(asm, src):
+    # Behind a buffer store of more than 8 bytes a lane with a scalar register
+    # in its offset the compiler keeps no distance to the next write of the
+    # stored registers, and such a write reached what some lanes store.
+    bad = re.findall(r"buffer_store_dwordx[34] [^\n]*, s\d+ offen", asm[src])
+    assert not bad, bad[:3]
+    if src in FILES[2:]:
+        assert re.search(r"buffer_store_dwordx4 [^\n]*, 0 offen", asm[src])
