@@ -367,3 +367,52 @@ def test_repeats_are_equal_bit_for_bit(cco, rows, n, k, groups):
         for i, o in enumerate(outs):
             differ[i] += (o != want[i]).sum()
     assert differ.tolist() == [0] * len(outs)
+
+
+@pytest.mark.parametrize("per,groups,n,k", [(30, 70, 2048, 2048), (3, 1000, 4096, 136),
+                                            (300, 1000, 1024, 128), (290, 900, 136, 1288)])
+def test_more_tiles_than_workgroups(cco, per, groups, n, k):
+    # workgroups take several tiles, full and wide ones in turn: a tile's
+    # first loads and the last tile's stores are in flight together
+    g = torch.Generator().manual_seed(per)
+    counts = (torch.randint(0, 2 * per + 1, (groups,), generator=g)).tolist()
+    first, count = _packed(counts)
+    rows = sum(counts)
+    f, c = _i32(first), _i32(count)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+
+    def r(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(BF)
+
+    x, dy, w = r(rows, k), r(rows, n), r(groups, n, k)
+    outs = [torch.empty((rows, n), dtype=BF, device="cuda"),
+            torch.empty((rows, k), dtype=BF, device="cuda"),
+            torch.empty((groups, n, k), dtype=BF, device="cuda"),
+            torch.empty((groups, n, k), dtype=F32, device="cuda")]
+
+    def run():
+        for o in outs:
+            o.fill_(float("nan"))
+        cco.group_product(f, c, x, w, out=outs[0])
+        cco.group_product_dx(f, c, dy, w, out=outs[1])
+        cco.group_product_dw(f, c, dy, x, out=outs[2])
+        cco.group_product_dw(f, c, dy, x, out=outs[3])
+
+    run()
+    want = [o.clone() for o in outs]
+    for e in (0, 1, groups // 2, groups - 2, groups - 1):
+        lo, hi = first[e], first[e] + count[e]
+        xs, ds, we = x[lo:hi].cpu(), dy[lo:hi].cpu(), w[e].cpu()
+        for i, (a, b, terms) in enumerate(((xs, we.t(), k), (ds, we, n), (ds.t(), xs, hi - lo),
+                                           (ds.t(), xs, hi - lo))):
+            v, s = ref.product(a, b)
+            got = want[i][lo:hi] if i < 2 else want[i][e]
+            ref.assert_within(got, v, ref.product_bound(v, s, terms, outs[i].dtype),
+                              "output %d group %d" % (i, e))
+    assert bool((want[3].to(BF) == want[2]).all())
+    differ = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for _ in range(15):
+        run()
+        for i, o in enumerate(outs):
+            differ[i] += (o != want[i]).sum()
+    assert differ.tolist() == [0] * 4
