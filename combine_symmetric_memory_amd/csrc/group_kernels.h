@@ -123,6 +123,7 @@ struct GenOperand {
 template <int OP, bool F16, bool OUT32, bool SHORT>
 __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a) {
   __shared__ __align__(16) char lds[2][2][kGenOperand];
+  static_assert(sizeof(lds) == kGenTile * kGenTile * 4, "the LDS holds one tile's results");
   constexpr bool AKC = OP != kGroupDw, BKC = OP == kGroupProduct;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int wm = wave / 2, wn = wave % 2;
@@ -206,29 +207,55 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
     }
     char *cbase = a.c + (OP == kGroupDw ? (int64_t)g * welems : gr.lo * a.ldc) * (OUT32 ? 4 : 2);
     const int64_t ldc = OP == kGroupDw ? a.k : a.ldc;
+    // Results through the (idle) LDS, so that a wavefront stores two
+    // neighbouring elements a lane along a row, whatever its alignment:
+    // stored from the accumulators' order, 2 bytes a lane over 32 rows, a
+    // weight gradient of few steps spent most of its time here.  Chunk c of
+    // 16 bytes of row r lies at c ^ (r % 32).
+    char *tile = &lds[0][0][0];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int row = row0 + wm * 64 + i * 32 + (lane & 31);
-          const int col = col0 + wn * 64 + j * 32 + q * 8 + (lane >> 5) * 4;
-          if (row >= out_rows) continue;
+          const int row = wm * 64 + i * 32 + (lane & 31);
+          const int c = wn * 16 + j * 8 + q * 2 + (lane >> 5);
+          f32x4 v;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (col + c >= ncol) continue;
-            char *p = cbase + (row * ldc + col + c) * (OUT32 ? 4 : 2);
-            float v = acc[i][j][4 * q + c];
-            if constexpr (OUT32) {
-              if (a.accumulate) v += *(float *)p;
-              *(float *)p = v;
-            } else {
-              if (a.accumulate) v += from_half_bits<F16>(*(uint16_t *)p);
-              *(uint16_t *)p = to_half_bits<F16>(v);
-            }
-          }
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          *(f32x4 *)(tile + row * 512 + ((c ^ (row & 31)) * 16)) = v;
         }
+    __syncthreads();
+    const int col = col0 + 2 * lane;
+    const int rows_here = (int)min((int64_t)kGenTile, (int64_t)out_rows - row0);
+    for (int row = wave; row < rows_here; row += kGenThreads / kWave) {
+      const char *at = tile + row * 512 + (((lane >> 1) ^ (row & 31)) * 16) + (lane & 1) * 8;
+      float v[2] = {((const float *)at)[0], ((const float *)at)[1]};
+      char *out = cbase + ((int64_t)(row0 + row) * ldc + col) * (OUT32 ? 4 : 2);
+      const int n = min(2, ncol - col);  // elements of this lane that exist
+      if (n <= 0) continue;
+      using E = std::conditional_t<OUT32, float, uint16_t>;
+      E e[2] = {0, 0};
+      if (a.accumulate) {
+        if (n == 2)
+          __builtin_memcpy(e, out, sizeof(e));
+        else
+          __builtin_memcpy(e, out, sizeof(E));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (OUT32)
+          e[i] = a.accumulate ? v[i] + e[i] : v[i];
+        else
+          e[i] = to_half_bits<F16>(a.accumulate ? v[i] + from_half_bits<F16>(e[i]) : v[i]);
+      }
+      if (n == 2)
+        __builtin_memcpy(out, e, sizeof(e));
+      else
+        __builtin_memcpy(out, e, sizeof(E));
+    }
+    __syncthreads();  // the tile is read out before the next one's operands come
   }
 }
 
