@@ -384,32 +384,47 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
       ry1 = rms_inverse(s[0], H, a.eps);
     }
     const float st = a.scale * tg;
-    // x becomes out, q becomes du pre; v = gate_channel post y
-    float s[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    // With pre x becomes out; v = gate_channel post y.  A norm that is not
+    // there leaves its row out of the sums and products: an infinity in it
+    // would come back as 0 * inf.
+    float vd;  // scale v . d, d with what comes through the norm of out
     const float sry = st * ry1;
+    if (a.pre) {
+      float s[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float v = gp[i] * y[i], qi = q[i] * pre[i];
-      x[i] = __builtin_fmaf(sry, v, x[i]);
-      s[0] = __builtin_fmaf(x[i], x[i], s[0]);
-      s[1] = __builtin_fmaf(qi, x[i], s[1]);
-      s[2] = __builtin_fmaf(v, d[i], s[2]);
-      s[3] = __builtin_fmaf(v, qi, s[3]);
-      s[4] = __builtin_fmaf(v, x[i], s[4]);
+      for (int i = 0; i < N; ++i) {
+        const float v = gp[i] * y[i], qi = q[i] * pre[i];
+        x[i] = __builtin_fmaf(sry, v, x[i]);
+        s[0] = __builtin_fmaf(x[i], x[i], s[0]);
+        s[1] = __builtin_fmaf(qi, x[i], s[1]);
+        s[2] = __builtin_fmaf(v, d[i], s[2]);
+        s[3] = __builtin_fmaf(v, qi, s[3]);
+        s[4] = __builtin_fmaf(v, x[i], s[4]);
+      }
+      block_sum<5>(s, lds, half, waves);
+      const float ro = rms_inverse(s[0], H, a.eps);
+      const float m3 = ro * ro * ro * s[1] * inv_h;  // ro^3 M
+      vd = a.scale * (s[2] + ro * s[3] - m3 * s[4]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dpre[i] = __builtin_fmaf(q[i] * ro, x[i], dpre[i]);
+        d[i] += ro * (q[i] * pre[i]) - x[i] * m3;
+      }
+    } else {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[0] = __builtin_fmaf(gp[i] * y[i], d[i], s[0]);
+      block_sum<1>(s, lds, half, waves);
+      vd = a.scale * s[0];
     }
-    block_sum<5>(s, lds, half, waves);
-    const float ro = a.pre ? rms_inverse(s[0], H, a.eps) : 0.0f;
-    const float m3 = ro * ro * ro * s[1] * inv_h;               // ro^3 M
-    const float vd = a.scale * (s[2] + ro * s[3] - m3 * s[4]);  // scale v . d
     if (token && threadIdx.x == 0) a.dgate[t] = vd * ry1;
-    const float by = a.post ? ry1 * ry1 * ry1 * tg * vd * inv_h : 0.0f;  // ry^3 mean(b y)
+    const float by = ry1 * ry1 * ry1 * tg * vd * inv_h;  // ry^3 mean(b y)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      dpre[i] = __builtin_fmaf(q[i] * ro, x[i], dpre[i]);
-      d[i] += ro * (q[i] * pre[i]) - x[i] * m3;
       const float sd = sry * d[i];
       csum[i] = __builtin_fmaf(sd, y[i], csum[i]);
-      q[i] = __builtin_fmaf(-y[i], by, sd * gp[i]);
+      q[i] = sd * gp[i];
+      if (a.post) q[i] = __builtin_fmaf(-y[i], by, q[i]);
     }
     store_row<END, T, NV>((T *)a.dx + off, H, d);
     if (a.dy) store_row<END, T, NV>((T *)a.dy + off, H, q);

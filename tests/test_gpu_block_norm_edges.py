@@ -1,0 +1,76 @@
+"""The norms around a block where their gradient is easily wrong: infinite
+and NaN rows that the formula does not read."""
+import math
+
+import pytest
+import torch
+
+from tests import test_gpu_block_norm as base
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def cco():
+    import combine_symmetric_memory_amd as m
+    assert torch.cuda.is_available()
+    return m
+
+
+def _equal(a, b):
+    return (a is None and b is None) or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("H", [520, 77, 5, 8200])
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("post,gate", [(True, "none"), (True, "channel"), (True, "token"),
+                                       (False, "none"), (False, "channel"), (False, "token")])
+def test_without_pre_the_gradient_does_not_read_x(cco, H, dtype, post, gate):
+    # out = x + scale gate z: no derivative of out depends on x
+    say("case: x outside the gradient H=%d %s post=%s gate=%s" % (H, dtype, post, gate))
+    d = base._inputs(6, H, dtype, F32, post, gate, False)
+    kw = dict(base._kw(d), scale=0.7, eps=EPS)
+    y, dout = d["y"].cuda(), d["dout"].cuda()
+    x = torch.zeros((6, H), dtype=dtype, device="cuda")
+    want = cco.block_norm_grad(x, y, dout, **kw)
+    for t in want:
+        assert t is None or bool(torch.isfinite(t).all())
+    x[0, 0] = math.inf
+    x[1, H - 1] = -math.inf
+    x[2, H // 2] = math.nan
+    x[3] = torch.finfo(dtype).max
+    x[4] = math.inf
+    got = cco.block_norm_grad(x, y, dout, **kw)
+    assert torch.equal(got[0], dout)
+    for g, w in zip(got, want):
+        assert _equal(g, w)
+
+
+@pytest.mark.parametrize("H", [520, 77, 5, 8200])
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+def test_without_norms_dy_does_not_read_y(cco, H, gate):
+    # z = y: dx = dout and dy = scale gate dout whatever y holds, and a gate's
+    # gradient meets only the columns or tokens that hold the infinities
+    d = base._inputs(6, H, BF, F32, False, gate, False)
+    kw = dict(base._kw(d), scale=0.7, eps=EPS)
+    x, y, dout = d["x"].cuda(), d["y"].cuda(), d["dout"].cuda()
+    want = cco.block_norm_grad(x, y, dout, **kw)
+    bad = y.clone()
+    bad[1, 0] = math.inf
+    bad[2, H - 1] = math.nan
+    bad[4] = torch.finfo(BF).max
+    got = cco.block_norm_grad(x, bad, dout, **kw)
+    assert torch.equal(got[0], dout) and torch.equal(got[1], want[1])
+    assert bool(torch.isfinite(got[1]).all())
+    if gate == "token":
+        good = [0, 3, 5]
+        assert torch.equal(got[3][good], want[3][good])
+        assert not bool(torch.isfinite(got[3][[1, 2]]).any())
+    if gate == "channel":
+        bad[4] = y[4]
+        got = cco.block_norm_grad(x, bad, dout, **kw)
+        assert torch.equal(got[3][1:H - 1], want[3][1:H - 1])
+        assert not bool(torch.isfinite(got[3][[0, H - 1]]).any())
