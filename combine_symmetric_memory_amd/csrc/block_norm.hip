@@ -5,14 +5,14 @@
 //   out = x + scale gate z
 //   u = out ro pre,                    ro = 1 / sqrt(mean out^2 + eps)
 //
-// Gradient, with q = du pre and M = mean(q out):
-//   d  = dout + ro q - out ro^3 M                              (dx)
+// Gradient, with q = du pre and M = mean(q out ro):
+//   d  = dout + ro (q - out ro M)                              (dx)
 //   dz = scale gate d,   dgate = scale z d (summed over the tokens or a row)
-//   dy = post ? ry b - y ry^3 mean(b y) : dz,   b = dz post
+//   dy = post ? ry (b - y ry mean(b y ry)) : dz,   b = dz post
 //   dpost = sum_t dz y ry,   dpre = sum_t du out ro
-// mean(b y) would be a third sum over the row that waits for M; it is linear
-// in d, so the row's second sum also carries v . dout, v . q and v . out
-// (v = scale gate post y) and mean(b y) follows from them.  With
+// mean(b y ry) would be a third sum over the row that waits for M; it is
+// linear in d, so the row's second sum also carries v . dout, v . q and
+// v . out (v = scale gate post y ry) and mean(b y ry) follows.  With
 // C = sum_t scale d y ry (times a token gate), dpost = gate C and a channel's
 // dgate = post C: one column sum serves both.
 //
@@ -384,17 +384,23 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
       ry1 = rms_inverse(s[0], H, a.eps);
     }
     const float st = a.scale * tg;
-    // With pre x becomes out; v = gate_channel post y.  A norm that is not
-    // there leaves its row out of the sums and products: an infinity in it
-    // would come back as 0 * inf.
+    // y becomes y ry.  With pre x becomes out and then out ro;
+    // v = gate_channel post y ry.  A norm that is not there leaves its row
+    // out of the sums and products: an infinity in it would come back as
+    // 0 * inf.  ry and ro meet the rows they normalise before anything else:
+    // their squares and cubes leave the range of fp32 long before the rows'
+    // sums of squares do.
     float vd;  // scale v . d, d with what comes through the norm of out
-    const float sry = st * ry1;
+    if (a.post) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] *= ry1;
+    }
     if (a.pre) {
       float s[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float v = gp[i] * y[i], qi = q[i] * pre[i];
-        x[i] = __builtin_fmaf(sry, v, x[i]);
+        x[i] = __builtin_fmaf(st, v, x[i]);
         s[0] = __builtin_fmaf(x[i], x[i], s[0]);
         s[1] = __builtin_fmaf(qi, x[i], s[1]);
         s[2] = __builtin_fmaf(v, d[i], s[2]);
@@ -403,12 +409,13 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
       }
       block_sum<5>(s, lds, half, waves);
       const float ro = rms_inverse(s[0], H, a.eps);
-      const float m3 = ro * ro * ro * s[1] * inv_h;  // ro^3 M
-      vd = a.scale * (s[2] + ro * s[3] - m3 * s[4]);
+      const float m = ro * s[1] * inv_h;  // ro M
+      vd = a.scale * (s[2] + ro * (s[3] - ro * s[4] * m));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        dpre[i] = __builtin_fmaf(q[i] * ro, x[i], dpre[i]);
-        d[i] += ro * (q[i] * pre[i]) - x[i] * m3;
+        const float xn = x[i] * ro;
+        dpre[i] = __builtin_fmaf(q[i], xn, dpre[i]);
+        d[i] = __builtin_fmaf(ro, __builtin_fmaf(-xn, m, q[i] * pre[i]), d[i]);
       }
     } else {
       float s[1] = {0.0f};
@@ -417,14 +424,14 @@ __global__ __launch_bounds__(MAXT) void norm_grad_kernel(NormArgs a) {
       block_sum<1>(s, lds, half, waves);
       vd = a.scale * s[0];
     }
-    if (token && threadIdx.x == 0) a.dgate[t] = vd * ry1;
-    const float by = ry1 * ry1 * ry1 * tg * vd * inv_h;  // ry^3 mean(b y)
+    if (token && threadIdx.x == 0) a.dgate[t] = vd;
+    const float by = tg * vd * inv_h;  // mean(b y ry)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float sd = sry * d[i];
+      const float sd = st * d[i];
       csum[i] = __builtin_fmaf(sd, y[i], csum[i]);
       q[i] = sd * gp[i];
-      if (a.post) q[i] = __builtin_fmaf(-y[i], by, q[i]);
+      if (a.post) q[i] = ry1 * __builtin_fmaf(-y[i], by, q[i]);
     }
     store_row<END, T, NV>((T *)a.dx + off, H, d);
     if (a.dy) store_row<END, T, NV>((T *)a.dy + off, H, q);

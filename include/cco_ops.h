@@ -149,7 +149,9 @@ typedef enum { CCO_GATE_NONE = 0, CCO_GATE_CHANNEL = 1, CCO_GATE_TOKEN = 2 } cco
  *   u   = out / rms(out) * pre   (of the unrounded out; with pre only)
  * post, pre, and a gate per channel are device [hidden] vectors of `wdtype`
  * (CCO_F32 or the rows' type); a gate per token is device fp32 [T].  post
- * and pre may be NULL. */
+ * and pre may be NULL.
+ * Sums of squares are fp32: a normalised row whose sum passes 2^128 becomes
+ * zeros, and one whose mean square lies below 2^-126 counts as eps alone. */
 typedef struct {
   int32_t hidden;    /* 1..16384 */
   int32_t dtype;     /* rows: CCO_BF16, CCO_F16 or CCO_F32 */

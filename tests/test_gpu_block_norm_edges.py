@@ -1,5 +1,5 @@
 """The norms around a block where their gradient is easily wrong: infinite
-and NaN rows that the formula does not read."""
+and NaN rows that the formula does not read, and rows far from one."""
 import math
 
 import pytest
@@ -74,3 +74,28 @@ def test_without_norms_dy_does_not_read_y(cco, H, gate):
         got = cco.block_norm_grad(x, bad, dout, **kw)
         assert torch.equal(got[3][1:H - 1], want[3][1:H - 1])
         assert not bool(torch.isfinite(got[3][[0, H - 1]]).any())
+
+
+@pytest.mark.parametrize("factor", [1e15, 3e16, 1e-14, 1e-17])
+@pytest.mark.parametrize("post,gate,pre", [f for f in base.FORMS if f[0] or f[2]])
+def test_rows_far_from_one(cco, monkeypatch, factor, post, gate, pre):
+    # x and y scaled by `factor` and dout by its inverse, eps 0: every term
+    # of the gradient keeps its share
+    plain = base._inputs
+
+    def scaled(T, H, dtype, *a, **kw):
+        d = plain(T, H, dtype, *a, **kw)
+        d["x"] = (d["x"].double() * factor).to(dtype)
+        if d["y"] is not None:
+            d["y"] = (d["y"].double() * factor).to(dtype)
+        d["dout"] = (d["dout"].double() / factor).to(dtype)
+        return d
+
+    monkeypatch.setattr(base, "_inputs", scaled)
+    monkeypatch.setattr(base, "EPS", 0.0)
+    # z is normalised with post and takes its size from scale, from y without
+    scale = 0.7 * (factor if post else 1.0)
+    for dtype, H in ((BF, 256), (F32, 77), (BF, 8200)):
+        base._check(cco, 5, H, dtype, F32, post, gate, pre, scale=scale)
+        if pre:
+            base._check(cco, 3, H, dtype, F32, post, gate, pre, scale=scale, use_dout=False)
