@@ -331,8 +331,30 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_grad_kernel(RouteArg
   }
 }
 
+// Tokens of one launch: with 64 lanes a token, 2^26 of them would need a
+// grid of 2^32 threads, which does not run as such.
+constexpr int32_t kLaunchTokens = 1 << 24;
+
 template <int DT, int EPL>
-hipError_t launch_route_as(bool grad, const RouteArgs &a, hipStream_t st) {
+hipError_t launch_route_as(bool grad, const RouteArgs &all, hipStream_t st) {
+  RouteArgs a = all;
+  if (a.T > kLaunchTokens) {
+    const int64_t size = DT == CCO_F32 ? 4 : 2;
+    for (int64_t t = 0; t < all.T; t += kLaunchTokens) {
+      a.T = (int32_t)std::min<int64_t>(kLaunchTokens, all.T - t);
+      a.logits = (const char *)all.logits + t * all.ld * size;
+      a.idx = all.idx + t * all.K;
+      if (grad) {
+        a.dw = all.dw + t * all.K;
+        a.dlogits = (char *)all.dlogits + t * all.lddl * size;
+      } else {
+        a.w = all.w + t * all.K;
+      }
+      const hipError_t err = launch_route_as<DT, EPL>(grad, a, st);
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   // few tokens: a workgroup each, so that they spread over the CUs
   const int waves = a.T < 4096 ? 1 : kRouteWaves;
   const dim3 grid((uint32_t)(((int64_t)a.T + waves - 1) / waves)), block(waves * kWave);
