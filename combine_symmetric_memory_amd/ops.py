@@ -100,9 +100,11 @@ def _rows(t: torch.Tensor, dev, name: str, cols: int | None = None, rows: int | 
         raise ValueError("%s must be [%s, %s], got %s" % (
             name, "rows" if rows is None else rows, "columns" if cols is None else cols,
             tuple(shape)))
+    r, c = shape
+    if r > _MAX_COUNT or c > _MAX_COUNT:
+        _counts(name, r, c)
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    r, c = shape
     if t.is_contiguous():
         return c or 1
     ld, step = t.stride()
@@ -115,6 +117,15 @@ def _rows(t: torch.Tensor, dev, name: str, cols: int | None = None, rows: int | 
     return ld or 1
 
 
+# The C entries take counts as int32, and ctypes would cut larger ones off.
+_MAX_COUNT = 2 ** 31 - 1
+
+
+def _counts(what: str, *sizes: int) -> None:
+    if max(sizes) > _MAX_COUNT or min(sizes) < -_MAX_COUNT:
+        raise ValueError("%s: %s does not fit an int32" % (what, max(sizes, key=abs)))
+
+
 def _p(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -123,6 +134,7 @@ def _p(t: torch.Tensor | None):
 def _route_desc(experts, topk, score, renorm, scale, groups=1, kept=1):
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
+    _counts("topk, groups and kept", int(topk), int(groups), int(kept))
     return _capi.cco_route_desc(int(experts), int(topk), _SCORES[score], int(bool(renorm)),
                                 float(scale), int(groups), int(kept))
 
@@ -192,6 +204,7 @@ def _groups(first, count, rows, dev):
     if not isinstance(first, torch.Tensor) or first.dim() != 1:
         raise ValueError("first must be int32 [groups]")
     n = first.shape[0]
+    _counts("first", n)
     _same(first, dev, "first", (n,), torch.int32)
     _same(count, dev, "count", (n,), torch.int32)
     return _capi.cco_groups(n, rows, first.data_ptr(), count.data_ptr())
@@ -219,6 +232,7 @@ def group_product(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, w: 
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("w must be [groups, n, k]")
     n = w.shape[1]
+    _counts("w", n)
     _same(w, dev, "w", (g.groups, n, k), x.dtype)
     if out is None:
         out = torch.empty((rows, n), dtype=x.dtype, device=dev)
@@ -245,6 +259,7 @@ def group_product_dx(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("w must be [groups, n, k]")
     k = w.shape[2]
+    _counts("w", k)
     _same(w, dev, "w", (g.groups, n, k), dy.dtype)
     if out is None:
         out = torch.empty((rows, k), dtype=dy.dtype, device=dev)
@@ -292,6 +307,8 @@ def _norm_desc(x: torch.Tensor, post, gate, token_gate, pre, scale, eps):
     if x.dim() != 2:
         raise ValueError("x must be [T, hidden]")
     T, H = x.shape
+    if T > _MAX_COUNT or H > _MAX_COUNT:
+        _counts("x", T, H)
     code = _dtype(x, "x")
     wdtype = None
     for name, v in (("post", post), ("pre", pre), ("gate", gate)):

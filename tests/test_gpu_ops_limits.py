@@ -1,5 +1,5 @@
 """The operators around the path at the ends of their ranges: more tokens than
-one launch has threads for."""
+one launch has threads for, and than an int32 counts."""
 import pytest
 import torch
 
@@ -37,3 +37,12 @@ def test_more_tokens_than_a_launch_has_threads(cco):
     bound = want * (ref.half_step(BF) + 32 * ref.U)
     assert bool(((torch.gather(got, 1, idx.long()).double() - want).abs() <= bound).all())
     assert not bool(torch.gather(got, 1, 1 - idx.long()).any())
+
+
+def test_tokens_past_the_counts_type_are_refused(cco):
+    # 2^32 + 5 rows are not 5 rows
+    x = torch.empty((2 ** 32 + 5, 1), dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        cco.route(x, 1)
+    with pytest.raises(ValueError):
+        cco.block_norm(x, pre=torch.ones(1, device="cuda"))
