@@ -188,6 +188,7 @@ class MoE:
         check(lib.cco_moe_get_routing(m, ctypes.byref(r)), "cco_moe_get_routing")
         self.routing_ptrs = r
         self.T = None
+        self._rows8 = False  # the receive windows hold 8-bit rows
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -213,6 +214,7 @@ class MoE:
         check(lib.cco_moe_dispatch(self.handle, _ptr(x, torch.bfloat16, "x"),
                                    _ptr(w, torch.float32, "w"), T, _stream(stream)),
               "cco_moe_dispatch")
+        self._rows8 = False
 
     def dispatch_fp8(self, x8: torch.Tensor, scales: torch.Tensor | None, w: torch.Tensor,
                      stream=None) -> None:
@@ -232,6 +234,7 @@ class MoE:
                                        _ptr(scales, torch.float32, "scales"), ns,
                                        _ptr(w, torch.float32, "w"), T, _stream(stream)),
               "cco_moe_dispatch_fp8")
+        self._rows8 = True
 
     def expert(self, w13: torch.Tensor | None, w2: torch.Tensor | None, stream=None) -> None:
         """cco_moe_expert; w13 bf16 [E, 2I, H], w2 bf16 [E, H, I]."""
@@ -290,6 +293,7 @@ class MoE:
                                 _ptr(out, torch.bfloat16, "out"), T, _stream(stream)),
               "cco_moe_fused")
         self.T = T
+        self._rows8 = False
         return out
 
     def stage_in_sdma(self, slot: int, src: torch.Tensor | int, rows: int, stream=None) -> None:
@@ -325,10 +329,15 @@ class MoE:
     def window(self, name: str, slot: int, rows: int) -> torch.Tensor:
         """The first `rows` rows of a slot's window as a bf16 tensor over the
         window's own memory (no copy): 'disp_x', 'hbuf' or 'out_tok'.
-        Borrowed: valid until the heap is destroyed."""
+        Borrowed: valid until the heap is destroyed.  'disp_x' is refused
+        after dispatch_fp8, whose rows are 8-bit codes and their scales (a
+        tensor taken before then shows their bytes); dispatch_view is their
+        address."""
         width = {"disp_x": self.H, "hbuf": self.I, "out_tok": self.H}
         if name not in width or getattr(self.layout, name + "_bytes") == 0:
             raise ValueError("no window %r in this layer" % name)
+        if name == "disp_x" and self._rows8:
+            raise ValueError("the receive windows hold 8-bit rows")
         if not 0 <= rows <= self.cap or not 0 <= slot < self.S:
             raise ValueError("slot or rows out of range")
         ptr = self.heap.slot_ptr(slot, getattr(self.layout, name))

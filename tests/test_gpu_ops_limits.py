@@ -1,10 +1,12 @@
 """The operators around the path at the ends of their ranges: more tokens than
-one launch has threads for, and than an int32 counts."""
+one launch has threads for and than an int32 counts, and windows that hold
+8-bit rows."""
+import numpy as np
 import pytest
 import torch
 
 from tests import ops_ref as ref
-from tests.gpu_util import say
+from tests.gpu_util import make_moe, say
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -46,3 +48,31 @@ def test_tokens_past_the_counts_type_are_refused(cco):
         cco.route(x, 1)
     with pytest.raises(ValueError):
         cco.block_norm(x, pre=torch.ones(1, device="cuda"))
+
+
+def test_window_of_8_bit_rows_is_refused(cco):
+    from synth import get_config
+    from synth.gen import activations, quantized_activations, routing
+    cfg = get_config("tiny")
+    idx, w = (torch.from_numpy(np.ascontiguousarray(v, t)).cuda()
+              for v, t in zip(routing(cfg), (np.int32, np.float32)))
+    x8, sc = (torch.from_numpy(v).cuda() for v in quantized_activations(cfg, None, block=64))
+    x = activations(cfg).cuda()
+    heap, moe = make_moe(cfg)
+    with heap:
+        moe.plan(idx)
+        moe.dispatch(x, w)
+        moe.window("disp_x", 0, 4)
+        moe.dispatch_fp8(x8, sc, w)
+        with pytest.raises(ValueError):
+            moe.window("disp_x", 0, 4)
+        with pytest.raises(ValueError):
+            moe.window("disp_x", 1, 0)
+        moe.window("out_tok", 0, 4)
+        moe.window("hbuf", 0, 4)
+        moe.dispatch(x, w)
+        first, count = moe.expert_groups(0)
+        rows = int(moe.status()[1][0])
+        xs = moe.window("disp_x", 0, rows)
+        tok = moe.read_rows("meta", 0, 0, rows)["src"] // cfg.K  # src is t * K + j
+        assert torch.equal(xs.cpu(), x.cpu()[torch.from_numpy(tok.astype(np.int64))])
