@@ -40,8 +40,10 @@ class _Elsewhere:
         self._dev, self._stream = dev, stream
 
     def __enter__(self):
-        self._stack.enter_context(torch.cuda.device(self._dev))
         s = self._stream
+        if isinstance(s, torch.cuda.Stream) and s.device != self._dev:
+            raise ValueError("the stream is on %s, the tensors on %s" % (s.device, self._dev))
+        self._stack.enter_context(torch.cuda.device(self._dev))
         if s is not None:
             if not isinstance(s, torch.cuda.Stream):
                 s = int(s)

@@ -1,5 +1,5 @@
 """Checks of the operators' binding that need no device: sizes past the types
-of the C entries."""
+of the C entries, and streams of another device."""
 import pytest
 import torch
 
@@ -37,3 +37,34 @@ def test_the_largest_sizes_pass_the_binding(ops):
     n = 2 ** 31 - 1
     assert ops._rows(_meta(n, 1), META, "x") == 1
     assert ops._rows(_meta(1, n), META, "x") == n
+
+
+def test_a_stream_of_another_device_is_refused(ops, monkeypatch):
+    # made current, it would take the call to its own device's default stream
+    class Stream:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    entered = []
+
+    class Context:
+        def __init__(self, what):
+            self.what = what
+
+        def __enter__(self):
+            entered.append(self.what)
+
+        def __exit__(self, *exc):
+            return False
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    dev = torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="stream"):
+        with ops._Elsewhere(dev, Stream(1)):
+            pass
+    assert not entered
+    s = Stream(0)
+    with ops._Elsewhere(dev, s):
+        assert entered == [dev, s]
