@@ -1,12 +1,13 @@
-"""The norms around a block where their gradient is easily wrong: infinite
-and NaN rows that the formula does not read, and rows far from one."""
+"""The norms around a block where they go wrong most easily: infinite and NaN
+rows that the gradient's formula does not read, rows far from one, and
+launches whose workgroups take several rows in every kernel form."""
 import math
 
 import pytest
 import torch
 
 from tests import test_gpu_block_norm as base
-from tests.gpu_util import say
+from tests.gpu_util import make_case, make_moe, say
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -99,3 +100,35 @@ def test_rows_far_from_one(cco, monkeypatch, factor, post, gate, pre):
         base._check(cco, 5, H, dtype, F32, post, gate, pre, scale=scale)
         if pre:
             base._check(cco, 3, H, dtype, F32, post, gate, pre, scale=scale, use_dout=False)
+
+
+# -------------------------------------- several rows a workgroup, every form
+@pytest.mark.parametrize("H,dtype", [(8200, BF), (9999, HF), (16384, BF), (12001, F32)])
+@pytest.mark.parametrize("post,gate", [(True, "channel"), (True, "token"), (False, "none")])
+def test_widest_rows_several_a_workgroup(cco, H, dtype, post, gate):
+    base._check(cco, 600, H, dtype, F32, post, gate, True)
+
+
+@pytest.mark.parametrize("config,over,T", [("dsv3", dict(), 1300), ("tiny", dict(H=256), 9000),
+                                           ("tiny", dict(H=8448), 700)])
+@pytest.mark.parametrize("post,gate,pre", [(True, "channel", True), (True, "token", True),
+                                           (False, "token", False), (False, "none", True)])
+def test_fused_combine_several_rows_a_workgroup(cco, config, over, T, post, gate, pre):
+    from synth import get_config
+    cfg = get_config(config).with_(I=0, **over)
+    say("case: combine_norm %s H=%d T=%d" % (config, cfg.H, T))
+    c = make_case(cfg, T)
+    heap, moe = make_moe(cfg, T)
+    with heap:
+        moe.plan(c.idx)
+        moe.dispatch(c.x, c.w)
+        y, _ = moe.combine(c.w)
+        d = base._inputs(T, cfg.H, BF, F32, post, gate, pre)
+        kw = dict(base._kw(d), scale=0.7, eps=EPS)
+        x = d["x"].cuda()
+        want = cco.block_norm(x, y, **kw)
+        for _ in range(3):
+            out, u, yy = cco.combine_norm(moe, x, c.w, keep_y=True, **kw)
+            assert torch.equal(yy, y) and torch.equal(out, want[0]) and _equal(u, want[1])
+            out, u, _ = cco.combine_norm(moe, x, c.w, **kw)
+            assert torch.equal(out, want[0]) and _equal(u, want[1])
