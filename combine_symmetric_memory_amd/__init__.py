@@ -4,7 +4,8 @@ MI355X (gfx950).
 The path runs in hand-written HIP kernels behind a C ABI (include/cco_moe.h,
 built into libcco_moe.so next to this file); this package is the Python
 binding.  The operators around the path (include/cco_ops.h) are functions:
-route, group_product and block_norm with their gradients, and combine_norm.  Importing it without the built library raises ImportError.
+route, group_product and block_norm with their gradients, and combine_norm.
+Importing it without the built library raises ImportError.
 """
 from ._capi import (  # noqa: F401
     CCO_ERR_BAD_EXPERT,

@@ -16,15 +16,17 @@
 // C = sum_t scale d y ry (times a token gate), dpost = gate C and a channel's
 // dgate = post C: one column sum serves both.
 //
-// Bound by memory (8192 x 7168 bf16, every operand present: 93 us forward,
-// 5.0 TB/s; gradient 143 us and 8 us of column sums, 4.9 TB/s of its rows):
-// every row is read once and stays in one workgroup's
-// registers, 16 elements a thread (8 for rows of at most 512).  Workgroups
-// walk the rows with the vectors in registers and the next row's loads in
-// flight while the present one is summed; as many workgroups as the
-// registers let run at once.  The gradient's column sums stay in registers
-// too, one partial per workgroup, added in workgroup order by a second
-// kernel (no atomics).
+// Bound by memory (8192 x 7168 bf16, every operand present, calls back to
+// back: 93 us forward, 5.1 TB/s; gradient with its column sums 138 us, 5.1
+// TB/s, of which the column sums' kernel is 5 us): every row is read once and
+// stays in one workgroup's registers, 16 elements a thread (8 for rows of at
+// most 512).  Workgroups walk the rows with the vectors in registers and the
+// next row's loads in flight while the present one is summed; as many
+// workgroups as the registers let run at once.  The gradient's column sums
+// stay in registers too, one partial per workgroup, added in workgroup order
+// by a second kernel (no atomics).  Past 8192 columns the gradient's threads
+// have half the registers, 264 to 488 bytes of scratch and no row in flight
+// ahead (2000 x 16384 bf16: 248 us, 1.6 TB/s; forward 47 us).
 #include "combine_impl.h"
 #include "ops_internal.h"
 #include "wave_ops.h"
@@ -194,7 +196,11 @@ __device__ __forceinline__ int uniform_int(int v) { return __builtin_amdgcn_read
 
 // A thread's share of combine's output row of token t, rounded to bf16: the
 // sum over the token's K pairs in order, as combine_token forms it.  (H is a
-// multiple of 8 and the windows are aligned.)
+// multiple of 8 and the windows are aligned.)  Bound by latency: a pair's id
+// and position are loads as well, and loads complete in order, so those of
+// the next pair wait for this pair's rows, K round trips a token.  Measured
+// with 7168 columns and 8 pairs, against the two launches it replaces: 256
+// tokens 12 and 17 us, 512 tokens 25 and 22 us, 8192 tokens 323 and 274 us.
 template <int NV>
 __device__ __forceinline__ void combine_row(const CombineView &c, int64_t t, int H,
                                             RowRaw<kWhole, __bf16, NV> &out) {
@@ -202,7 +208,7 @@ __device__ __forceinline__ void combine_row(const CombineView &c, int64_t t, int
   float y[NV * 8];
 #pragma unroll
   for (int i = 0; i < NV * 8; ++i) y[i] = 0.0f;
-  constexpr int B = 8;  // pairs whose rows are in flight together
+  constexpr int B = 8;  // pairs summed together
   for (int j0 = 0; j0 < a.K; j0 += B) {
     u32x4 r[B][NV];
     float w[B];
@@ -456,8 +462,8 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(NormArgs a, int nwg) {
   const int h = blockIdx.x * kWave + lane;
   float s = 0.0f;
   if (h < a.H) {
-    // eight loads in flight a chain (one after the other, 1789 partials of
-    // 360 columns took 30 us)
+    // eight loads in flight a chain: one after the other each would wait
+    // out a round trip
     int w = chain;
     for (; w + 7 * 16 < nwg; w += 8 * 16) {
       float v[8];

@@ -26,10 +26,11 @@
 // PFLOP/s, one group of 65536 rows by 4096 x 4096, dw 1.28 (bound by the
 // matrix cores' clock under load and the operands' way through LDS, no bank
 // conflicts); 256 groups of 8 rows by 7168 x 2048, product 5.9 TB/s of
-// weights.  A tile's results and first loads cost about 17000 cycles of the
-// 3400 a step takes, so reductions of few steps stay below (16 steps: 1.0
-// PFLOP/s, with fp32 results 0.87: loads and stores complete in one order,
-// and the third step waits for the last tile's stores).
+// weights.  A tile's results and first loads cost about 17000 cycles, a step
+// about 3400, so reductions of few steps stay below (16 steps: 1.08 PFLOP/s,
+// with fp32 results 0.85 to 0.94: loads and stores complete in one order, A's
+// step 1 is loaded behind the last tile's stores, and so the second step
+// waits for them).
 //
 // A step is four MFMA sub-steps on two fragment buffers in turn: while one
 // is multiplied the other is read, and the loads of a later step are spread

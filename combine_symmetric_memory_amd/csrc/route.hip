@@ -11,8 +11,8 @@
 // values next to a border do not change places by rounding.
 //
 // Latency and issue bound, not memory: 16384 tokens of 256 fp32 logits, top
-// 8, take 15.5 us for 18 MB (the gradient 12.6 us for 35 MB); 256 tokens
-// with 8 groups 8.7 us, of which the launch itself is about 4.  (Reductions
+// 8, take 15.2 us for 18 MB (the gradient 12.9 us for 35 MB); 256 tokens
+// with 8 groups 8.5 us, of which the launch itself is about 4.  (Reductions
 // through LDS permutes took 37 and 12.2 us.)
 #include "ops_internal.h"
 #include "wave_ops.h"

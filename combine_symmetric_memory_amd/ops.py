@@ -13,6 +13,9 @@ the router, the products grouped by expert and the norms around a block.
 Arguments are checked and marshalled here, the work is in the library's HIP
 kernels.  Calls run on the tensors' device, on torch's current stream of it
 unless `stream` is given; outputs that are not passed are made by torch.
+Nothing is recorded for automatic differentiation, whatever the inputs
+require: results carry no gradient, the calls named _grad, _dx and _dw
+compute it.
 """
 from __future__ import annotations
 
@@ -409,7 +412,9 @@ def combine_norm(moe: MoE, x: torch.Tensor, w: torch.Tensor, *, post: torch.Tens
                  keep_y: bool = False, stream=None):
     """cco_moe_combine_norm -> (out, u, y): MoE.combine of the staging views
     and block_norm of its result in one launch; y, the combined rows, only
-    with keep_y (None otherwise).  x bf16 [T, hidden], w fp32 [T, K]."""
+    with keep_y (None otherwise).  x bf16 [T, hidden], w fp32 [T, K].  For
+    decoding batches; from some hundreds of tokens on the two calls are
+    faster."""
     dev = _device(x, "x")
     if _away(dev, stream):
         with _Elsewhere(dev, stream):
