@@ -4,7 +4,9 @@ MI355X (gfx950).
 The path runs in hand-written HIP kernels behind a C ABI (include/cco_moe.h,
 built into libcco_moe.so next to this file); this package is the Python
 binding.  The operators around the path (include/cco_ops.h) are functions:
-route, group_product and block_norm with their gradients, and combine_norm.
+route, group_product and block_norm with their gradients, combine_norm,
+quant_rows, quant_swiglu and group_product_i8 in 8 bits, and moe_few, a whole
+layer for a few tokens.
 Importing it without the built library raises ImportError.
 """
 from ._capi import (  # noqa: F401
@@ -33,6 +35,10 @@ from .ops import (  # noqa: F401
     group_product,
     group_product_dw,
     group_product_dx,
+    group_product_i8,
+    moe_few,
+    quant_rows,
+    quant_swiglu,
     route,
     route_grad,
 )

@@ -25,7 +25,7 @@ CCO_ERR_DISABLED = -9
 CCO_NUM_KERNEL_KINDS = 10
 KERNEL_KINDS = ("plan_count", "plan_rank", "dispatch", "expert_gate_up", "expert_down",
                 "combine", "combine_copy_in", "dispatch_fp8", "stage_in_sdma", "fused")
-CCO_BF16, CCO_F16, CCO_F32 = 0, 1, 2
+CCO_BF16, CCO_F16, CCO_F32, CCO_I8 = 0, 1, 2, 3
 CCO_SCORE_SOFTMAX, CCO_SCORE_SIGMOID = 0, 1
 CCO_GROUP_PRODUCT, CCO_GROUP_DX, CCO_GROUP_DW = 0, 1, 2
 CCO_GATE_NONE, CCO_GATE_CHANNEL, CCO_GATE_TOKEN = 0, 1, 2
@@ -66,6 +66,13 @@ class cco_block_norm_desc(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32),
                 ("gate_kind", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
                 ("post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("pre", ctypes.c_void_p)]
+
+
+class cco_few_desc(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32),
+                ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("wdtype", ctypes.c_int32), ("w13", ctypes.c_void_p),
+                ("w2", ctypes.c_void_p), ("s13", ctypes.c_void_p), ("s2", ctypes.c_void_p)]
 
 
 # (name, restype, argtypes) for every symbol the header declares
@@ -109,6 +116,12 @@ SIGNATURES = [
     ("cco_block_norm_grad_workspace", U64, [P, I32]),
     ("cco_block_norm_grad", ctypes.c_int, [P, P, P, P, P, I32, P, P, P, P, P, P, U64, P]),
     ("cco_moe_combine_norm", ctypes.c_int, [P, P, P, P, I32, P, P, P, P]),
+    ("cco_quant_rows", ctypes.c_int, [P, I32, I64, I32, I32, I32, P, I64, P, I64, P]),
+    ("cco_group_product_i8_workspace", U64, [P, I32, I32]),
+    ("cco_group_product_i8", ctypes.c_int, [P, P, I64, P, I64, P, P, I32, I32, P, I32, I64, P,
+                                            U64, P]),
+    ("cco_moe_few_workspace", U64, [P, I32]),
+    ("cco_moe_few", ctypes.c_int, [P, P, P, P, I32, P, P, U64, P]),
     ("cco_status_string", ctypes.c_char_p, [ctypes.c_int]),
 ]
 

@@ -89,16 +89,43 @@ struct TileMap {
   }
 };
 
+// The operands' elements and the sums they give.  8-bit ones stand two to
+// each 16 bits of the reduction: the same bytes in the same places.
+enum GroupElem { kElemBf16, kElemF16, kElemI8 };
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+template <GroupElem EL>
+struct GroupAcc {
+  using type = f32x16;
+};
+template <>
+struct GroupAcc<kElemI8> {
+  using type = i32x16;
+};
+
 // One MFMA, C^T += B A^T: lane l ends up with row l % 32 of the block and
 // columns 8 (v / 4) + 4 (l / 32) + v % 4.
-template <bool F16>
-__device__ __forceinline__ f32x16 mfma_32x32x16(u32x4 b, u32x4 a, f32x16 c) {
-  if constexpr (F16)
+template <GroupElem EL>
+__device__ __forceinline__ typename GroupAcc<EL>::type group_mfma(
+    u32x4 b, u32x4 a, typename GroupAcc<EL>::type c) {
+  if constexpr (EL == kElemI8)
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, b),
+                                                 __builtin_bit_cast(i32x4, a), c, 0, 0, 0);
+  else if constexpr (EL == kElemF16)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b),
                                                   __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
   else
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
                                                    __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+}
+
+// An 8-bit product's result in fp32, the same in every kernel.  (Left to
+// itself the compiler rounds the last product and the conversion to fp16 at
+// once in some of them.)
+__device__ __forceinline__ float scaled_sum(float sum, float row, float column) {
+  float v = sum * row * column;
+  asm("" : "+v"(v));
+  return v;
 }
 
 template <bool F16>

@@ -35,8 +35,12 @@ constexpr int kGenOperand = kGenTile * kGenStep * 2;  // bytes of one operand's 
 // one and the column to the row's last eight; `put`, which runs once the
 // loads are in, moves down what a chunk at the row's end has, and puts zeros
 // outside.  SHORT: rows of fewer than eight, element by element.
-template <bool KC, bool SHORT>
+// 8-bit elements (I8; KC only) come sixteen to a chunk and 128 to a step.
+template <bool KC, bool SHORT, bool I8>
 struct GenOperand {
+  static_assert(KC || !I8, "8-bit operands are k-contiguous");
+  static constexpr int EB = I8 ? 1 : 2, CE = 16 / EB;  // bytes an element, elements a chunk
+  static constexpr int STEP = kGenStep * 2 / EB;
   const char *base;
   int64_t ld, nr;
   int32_t nc;
@@ -49,19 +53,28 @@ struct GenOperand {
     return (q * kGenThreads + (int)threadIdx.x) / (KC ? 8 : 16);
   }
   __device__ __forceinline__ int chunk_col(int q, int64_t k0) const {
-    const int c = (q * kGenThreads + (int)threadIdx.x) % (KC ? 8 : 16) * 8;
+    const int c = (q * kGenThreads + (int)threadIdx.x) % (KC ? 8 : 16) * CE;
     return KC ? (int)k0 + c : col0 + c;
   }
 
   __device__ __forceinline__ void fetch(int64_t k0) {
     const int64_t first = KC ? row0 : k0;  // uniform: the rows' base
-    const char *rows = base + first * ld * 2;
+    const char *rows = base + first * ld * EB;
     const int last = (int)min((int64_t)(kGenTile - 1), nr - 1 - first);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t row = (uint32_t)min(chunk_row(q), last) * (uint32_t)ld;
       const int c = chunk_col(q, k0);
-      if constexpr (SHORT) {
+      if constexpr (SHORT && I8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            v |= (uint32_t)(uint8_t)rows[row + (uint32_t)min(c + 4 * i + b, nc - 1)] << (8 * b);
+          stage[q][i] = v;
+        }
+      } else if constexpr (SHORT) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint16_t lo, hi;
@@ -70,7 +83,7 @@ struct GenOperand {
           stage[q][i] = (uint32_t)lo | ((uint32_t)hi << 16);
         }
       } else {
-        __builtin_memcpy(&stage[q], rows + (row + (uint32_t)min(c, nc - 8)) * 2, 16);
+        __builtin_memcpy(&stage[q], rows + (row + (uint32_t)min(c, nc - CE)) * EB, 16);
       }
     }
   }
@@ -80,12 +93,12 @@ struct GenOperand {
     uint64_t lo = v.x | ((uint64_t)v.y << 32), hi = v.z | ((uint64_t)v.w << 32);
     if constexpr (SHORT) {
       // keep the nc - c elements that exist
-      const int keep = max(0, min(8, nc - c)) * 16;
+      const int keep = max(0, min(CE, nc - c)) * (8 * EB);
       lo = keep >= 64 ? lo : lo & ((1ull << keep) - 1);
       hi = keep >= 128 ? hi : (keep <= 64 ? 0 : hi & ((1ull << (keep - 64)) - 1));
-    } else if (c + 8 > nc) {
-      // loaded from nc - 8: the first 8 - nc % 8 elements are before it
-      const int sh = (8 - nc % 8) * 16;
+    } else if (c + CE > nc) {
+      // loaded from nc - CE: the first CE - nc % CE elements are before it
+      const int sh = (CE - nc % CE) * (8 * EB);
       lo = sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
       hi = sh >= 64 ? 0 : hi >> sh;
     }
@@ -94,8 +107,8 @@ struct GenOperand {
   }
   __device__ __forceinline__ void put(char *lds, int64_t k0) const {
     // only steps and tiles at the matrix' edges need cutting
-    const bool edge = (KC ? row0 + kGenTile : k0 + kGenStep) > nr ||
-                      (KC ? k0 + kGenStep : (int64_t)col0 + kGenTile) > nc || SHORT;
+    const bool edge = (KC ? row0 + kGenTile : k0 + STEP) > nr ||
+                      (KC ? k0 + STEP : (int64_t)col0 + kGenTile) > nc || SHORT;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int i = q * kGenThreads + threadIdx.x;
@@ -120,8 +133,10 @@ struct GenOperand {
   }
 };
 
-template <int OP, bool F16, bool OUT32, bool SHORT>
+// (EL, F16 and OUT32 as in run_group_tile)
+template <int OP, GroupElem EL, bool F16, bool OUT32, bool SHORT>
 __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a) {
+  constexpr bool I8 = EL == kElemI8;
   __shared__ __align__(16) char lds[2][2][kGenOperand];
   static_assert(sizeof(lds) == kGenTile * kGenTile * 4, "the LDS holds one tile's results");
   constexpr bool AKC = OP != kGroupDw, BKC = OP == kGroupProduct;
@@ -141,11 +156,12 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
     const GroupRows gr = group_rows(a, g);
     const int row0 = r / ct * kGenTile, col0 = r % ct * kGenTile;
     const int64_t welems = (int64_t)a.n * a.k;
-    GenOperand<AKC, SHORT> oa;
-    GenOperand<BKC, SHORT> ob;
+    GenOperand<AKC, SHORT, I8> oa;
+    GenOperand<BKC, SHORT, I8> ob;
+    constexpr int EB = oa.EB, STEP = oa.STEP;
     int64_t kdim;       // reduction length
     int32_t out_rows;   // rows of this group's output
-    oa.base = a.a + gr.lo * a.lda * 2;
+    oa.base = a.a + gr.lo * a.lda * EB;
     oa.ld = a.lda;
     oa.nr = gr.n;
     oa.nc = OP == kGroupProduct ? a.k : a.n;
@@ -158,20 +174,20 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
     } else {
       kdim = oa.nc;
       out_rows = gr.n;
-      ob.base = a.b + (int64_t)g * welems * 2;
+      ob.base = a.b + (int64_t)g * welems * EB;
       ob.nr = a.n;
     }
     ob.ld = a.ldb;
     ob.nc = a.k;
     ob.row0 = ob.col0 = col0;
-    f32x16 acc[2][2];
+    typename GroupAcc<EL>::type acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    const int64_t steps = (kdim + kGenStep - 1) / kGenStep;
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    const int64_t steps = (kdim + STEP - 1) / STEP;
     if (steps > 0) {
       oa.fetch(0);
       ob.fetch(0);
@@ -182,8 +198,8 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
     for (int64_t s = 0; s < steps; ++s) {
       const int cur = (int)(s & 1);
       if (s + 1 < steps) {
-        oa.fetch((s + 1) * kGenStep);
-        ob.fetch((s + 1) * kGenStep);
+        oa.fetch((s + 1) * STEP);
+        ob.fetch((s + 1) * STEP);
       }
 #pragma unroll
       for (int sk = 0; sk < 4; ++sk) {
@@ -196,12 +212,12 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = mfma_32x32x16<F16>(fb[j], fa[i], acc[i][j]);
+          for (int j = 0; j < 2; ++j) acc[i][j] = group_mfma<EL>(fb[j], fa[i], acc[i][j]);
       }
       // the other buffer was last read in step s - 1, before its barrier
       if (s + 1 < steps) {
-        oa.put(lds[cur ^ 1][0], (s + 1) * kGenStep);
-        ob.put(lds[cur ^ 1][1], (s + 1) * kGenStep);
+        oa.put(lds[cur ^ 1][0], (s + 1) * STEP);
+        ob.put(lds[cur ^ 1][1], (s + 1) * STEP);
       }
       __syncthreads();
     }
@@ -223,15 +239,25 @@ __global__ __launch_bounds__(kGenThreads) void group_general_kernel(GroupArgs a)
           const int c = wn * 16 + j * 8 + q * 2 + (lane >> 5);
           f32x4 v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e];
           *(f32x4 *)(tile + row * 512 + ((c ^ (row & 31)) * 16)) = v;
         }
     __syncthreads();
     const int col = col0 + 2 * lane;
     const int rows_here = (int)min((int64_t)kGenTile, (int64_t)out_rows - row0);
+    float cs[2] = {1.0f, 1.0f};
+    if constexpr (I8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) cs[i] = a.cs[(int64_t)g * a.n + min(col + i, ncol - 1)];
+    }
     for (int row = wave; row < rows_here; row += kGenThreads / kWave) {
       const char *at = tile + row * 512 + (((lane >> 1) ^ (row & 31)) * 16) + (lane & 1) * 8;
       float v[2] = {((const float *)at)[0], ((const float *)at)[1]};
+      if constexpr (I8) {
+        const float rs = a.rs[(gr.lo + row0 + row) * a.ldrs];
+        v[0] = scaled_sum(v[0], rs, cs[0]);
+        v[1] = scaled_sum(v[1], rs, cs[1]);
+      }
       char *out = cbase + ((int64_t)(row0 + row) * ldc + col) * (OUT32 ? 4 : 2);
       const int n = min(2, ncol - col);  // elements of this lane that exist
       if (n <= 0) continue;
@@ -271,7 +297,7 @@ using WideTile = TileShape<OP != kGroupDw, OP == kGroupProduct, 128, 512, 2, 4>;
 
 // SPLIT: the reduction in a.parts parts, neighbouring units of a tile, whose
 // fp32 sums go to the workspace (then OUT32).
-template <int OP, bool F16, bool OUT32, bool ACC, int TILE, bool SPLIT>
+template <int OP, GroupElem EL, bool F16, bool OUT32, bool ACC, int TILE, bool SPLIT>
 __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_tile_kernel(
     GroupArgs a) {
   constexpr int ES = OUT32 ? 4 : 2;
@@ -351,6 +377,11 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
       t.c += ((lo + row0) * ldc + col0) * ES;
       t.c_rows = t.a_rows;
       t.c_cols = t.b_rows;
+      if constexpr (EL == kElemI8) {
+        t.rs = a.rs + (lo + row0) * a.ldrs;
+        t.ldrs = a.ldrs;
+        t.cs = a.cs + (int64_t)g * a.n + col0;
+      }
     }
     if constexpr (SPLIT) {
       // this part's steps (none: it leaves zeros)
@@ -383,10 +414,10 @@ __global__ __launch_bounds__(kGemmWaves *kWave, TILE == 128 ? 2 : 1) void group_
     };
     if constexpr (WIDE)
       if (wide) {
-        stored = run_group_tile<Wide, F16, OUT32, ACC>(now, smem, stored, next);
+        stored = run_group_tile<Wide, EL, F16, OUT32, ACC, SPLIT>(now, smem, stored, next);
         continue;
       }
-    stored = run_group_tile<Full, F16, OUT32, ACC>(now, smem, stored, next);
+    stored = run_group_tile<Full, EL, F16, OUT32, ACC, SPLIT>(now, smem, stored, next);
   }
 }
 
@@ -430,19 +461,19 @@ bool small_tiles(const GroupArgs &a) {
   return 3 * even_tiles((GroupOp)OP, 256, a.groups, a.rows, a.n, a.k) < 2 * kNumCus;
 }
 
-template <int OP, bool F16, bool OUT32>
+template <int OP, GroupElem EL, bool F16, bool OUT32>
 hipError_t launch_general(const GroupArgs &a, hipStream_t st) {
   const int64_t tiles = tile_bound<OP, kGenTile>(a);
   if (tiles == 0) return hipSuccess;
   const dim3 grid((uint32_t)std::min(tiles, kMaxGrid)), block(kGenThreads);
-  if (a.n < 8 || a.k < 8)
-    hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32, true>), grid, block, 0, st, a);
+  if (EL == kElemI8 ? a.k < 16 : a.n < 8 || a.k < 8)
+    hipLaunchKernelGGL((group_general_kernel<OP, EL, F16, OUT32, true>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((group_general_kernel<OP, F16, OUT32, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((group_general_kernel<OP, EL, F16, OUT32, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
-template <int OP, bool F16, bool OUT32, int TILE>
+template <int OP, GroupElem EL, bool F16, bool OUT32, int TILE>
 hipError_t launch_tiles(const GroupArgs &a, hipStream_t st) {
   const int64_t tiles = tile_bound<OP, TILE>(a);
   if (tiles == 0) return hipSuccess;
@@ -451,16 +482,17 @@ hipError_t launch_tiles(const GroupArgs &a, hipStream_t st) {
   const dim3 g((uint32_t)grid), b(kGemmWaves * kWave);
   constexpr int lds = FullTile<OP, TILE>::LDS_BYTES;
   if (OP == kGroupDw && a.accumulate)
-    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, OP == kGroupDw, TILE, false>), g, b, lds,
-                       st, a);
+    hipLaunchKernelGGL((group_tile_kernel<OP, EL, F16, OUT32, OP == kGroupDw, TILE, false>), g, b,
+                       lds, st, a);
   else
-    hipLaunchKernelGGL((group_tile_kernel<OP, F16, OUT32, false, TILE, false>), g, b, lds, st, a);
+    hipLaunchKernelGGL((group_tile_kernel<OP, EL, F16, OUT32, false, TILE, false>), g, b, lds, st,
+                       a);
   return hipGetLastError();
 }
 
 // C = the parts' sums, in order (dw: added to what is there).  Block y is a
 // group; its elements of a part are contiguous, rows of C columns.
-template <int OP, bool F16, bool OUT32>
+template <int OP, GroupElem EL, bool F16, bool OUT32>
 __global__ __launch_bounds__(256) void group_parts_kernel(GroupArgs a) {
   const int g = blockIdx.y;
   const int64_t cols = OP == kGroupProduct ? a.n : a.k;
@@ -475,9 +507,19 @@ __global__ __launch_bounds__(256) void group_parts_kernel(GroupArgs a) {
   // four elements a thread (columns are a multiple of 8)
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n * cols;
        i += (int64_t)gridDim.x * 1024) {
-    f32x4 s = *(const f32x4 *)(ws + i);
-    for (int p = 1; p < a.parts; ++p) s += *(const f32x4 *)(ws + p * part + i);
+    using Sum = std::conditional_t<EL == kElemI8, i32x4, f32x4>;
+    Sum sum = *(const Sum *)(ws + i);
+    for (int p = 1; p < a.parts; ++p) sum += *(const Sum *)(ws + p * part + i);
     const int64_t row = lo + i / cols, col = i % cols;
+    f32x4 s;
+    if constexpr (EL == kElemI8) {
+      const float rs = a.rs[row * a.ldrs];
+      const f32x4 cs = *(const f32x4 *)(a.cs + (int64_t)g * cols + col);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = scaled_sum((float)sum[e], rs, cs[e]);
+    } else {
+      s = sum;
+    }
     char *c = a.c + (row * (OP == kGroupDw ? cols : a.ldc) + col) * (OUT32 ? 4 : 2);
     if constexpr (OUT32) {
       if (a.accumulate) s += *(const f32x4 *)c;
@@ -499,40 +541,40 @@ __global__ __launch_bounds__(256) void group_parts_kernel(GroupArgs a) {
   }
 }
 
-template <int OP, bool F16, bool OUT32>
+template <int OP, GroupElem EL, bool F16, bool OUT32>
 hipError_t launch_split(const GroupArgs &a, hipStream_t st) {
   const int64_t tiles = tile_bound<OP, 128>(a);
   if (tiles == 0) return hipSuccess;
   const int64_t units = tiles * a.parts;
   const int64_t grid = std::min((units + kNumXcd - 1) / kNumXcd * kNumXcd, kMaxGrid);
-  hipLaunchKernelGGL((group_tile_kernel<OP, F16, true, false, 128, true>), dim3((uint32_t)grid),
+  hipLaunchKernelGGL((group_tile_kernel<OP, EL, F16, true, false, 128, true>), dim3((uint32_t)grid),
                      dim3(kGemmWaves * kWave), (FullTile<OP, 128>::LDS_BYTES), st, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int64_t cols = OP == kGroupProduct ? a.n : a.k;
   const int64_t elems = OP == kGroupDw ? a.n * cols : (a.rows + a.groups - 1) / a.groups * cols;
   const int64_t gx = std::min<int64_t>(std::max<int64_t>(1, (elems + 1023) / 1024), 1024);
-  hipLaunchKernelGGL((group_parts_kernel<OP, F16, OUT32>), dim3((uint32_t)gx, a.groups), dim3(256),
+  hipLaunchKernelGGL((group_parts_kernel<OP, EL, F16, OUT32>), dim3((uint32_t)gx, a.groups), dim3(256),
                      0, st, a);
   return hipGetLastError();
 }
 
-template <int OP, bool F16, bool OUT32>
+template <int OP, GroupElem EL, bool F16, bool OUT32>
 hipError_t launch_either(bool aligned, const GroupArgs &a, hipStream_t st) {
-  if (!aligned) return launch_general<OP, F16, OUT32>(a, st);
-  if (a.parts > 1) return launch_split<OP, F16, OUT32>(a, st);
-  return small_tiles<OP>(a) ? launch_tiles<OP, F16, OUT32, 128>(a, st)
-                            : launch_tiles<OP, F16, OUT32, 256>(a, st);
+  if (!aligned) return launch_general<OP, EL, F16, OUT32>(a, st);
+  if (a.parts > 1) return launch_split<OP, EL, F16, OUT32>(a, st);
+  return small_tiles<OP>(a) ? launch_tiles<OP, EL, F16, OUT32, 128>(a, st)
+                            : launch_tiles<OP, EL, F16, OUT32, 256>(a, st);
 }
 
 template <int OP>
 hipError_t launch_op(bool f16, bool out_f32, bool aligned, const GroupArgs &a, hipStream_t st) {
   if constexpr (OP == kGroupDw)
     if (out_f32)
-      return f16 ? launch_either<OP, true, true>(aligned, a, st)
-                 : launch_either<OP, false, true>(aligned, a, st);
-  return f16 ? launch_either<OP, true, false>(aligned, a, st)
-             : launch_either<OP, false, false>(aligned, a, st);
+      return f16 ? launch_either<OP, kElemF16, true, true>(aligned, a, st)
+                 : launch_either<OP, kElemBf16, false, true>(aligned, a, st);
+  return f16 ? launch_either<OP, kElemF16, true, false>(aligned, a, st)
+             : launch_either<OP, kElemBf16, false, false>(aligned, a, st);
 }
 
 }  // namespace

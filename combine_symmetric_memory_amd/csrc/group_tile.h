@@ -56,6 +56,8 @@ struct GroupTile {
   char *c;              // the tile's first output element
   int64_t ldc;          // bytes
   int32_t c_rows, c_cols;  // rows and columns of the tile that exist
+  const float *rs, *cs;    // 8-bit operands: scales of the tile's rows and columns
+  int64_t ldrs;            // distance of the rows' scales
 };
 
 // One operand's direct loads: W rows (k-contiguous) or columns (k-major).
@@ -240,9 +242,14 @@ constexpr int kTileStores = Shape::FB * Shape::FB * (OUT32 ? 4 : 2);
 // loads (false: any number).  next(): called once the operands are used up
 // and the rings are idle; it issues the next tile's first loads, which then
 // run while this tile's results are stored.
-template <class Shape, bool F16, bool OUT32, bool ACC, class Next>
+// EL: the operands' elements; F16: the results', unless OUT32.  With 8-bit
+// elements (two to each 16 bits of the reduction, sums in int32) a result is
+// the sum times its row's and its column's scale; RAW: the sum as it is.
+template <class Shape, GroupElem EL, bool F16, bool OUT32, bool ACC, bool RAW, class Next>
 __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, bool stored_before,
                                                Next &&next) {
+  constexpr bool SCALED = EL == kElemI8 && !RAW;
+  using Acc = typename GroupAcc<EL>::type;
   constexpr int WM = Shape::WM, WN = Shape::WN, FM = Shape::FB, FN = Shape::FB;
   constexpr int RB = Shape::RB;
   using LdA = typename Shape::LdA;
@@ -270,13 +277,40 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
   auto k_loop = [&](auto nact_c) __attribute__((always_inline)) {
     constexpr int NACT = decltype(nact_c)::value;
     constexpr int NF = NACT > 0 ? NACT : 1;
-    f32x16 acc[NF][FN];
+    Acc acc[NF][FN];
 #pragma unroll
     for (int i = 0; i < NF; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    // This lane's scales, in flight during the reduction: its row of every
+    // row block, and the columns 8 q + 4 (lane / 32) .. of every column block.
+    // (Rows and columns that do not exist take the last ones'.)
+    float rs[NF];
+    f32x4 cs[FN][4];
+    if constexpr (SCALED && NACT > 0) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+        rs[i] = t.rs[min((wm + i * WM) * 32 + (lane & 31), t.c_rows - 1) * t.ldrs];
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          cs[j][q] = *(const f32x4 *)(t.cs + min((wn * FN + j) * 32 + q * 8 + (lane >> 5) * 4,
+                                                 t.c_cols - 4));
+    }
+    // result v of block i, j
+    auto value = [&](auto i_c, auto j_c, int v) __attribute__((always_inline)) -> float {
+      constexpr int i = decltype(i_c)::value, j = decltype(j_c)::value;
+      if constexpr (SCALED)
+        return scaled_sum((float)acc[i][j][v], rs[i], cs[j][v / 4][v % 4]);
+      const auto sum = acc[i][j][v];  // (a bit cast of the element itself takes the first one's)
+      if constexpr (EL == kElemI8)
+        return __builtin_bit_cast(float, sum);
+      else
+        return sum;
+    };
     // fragments of two sub-steps; read order: B's, then A's
     u32x4 fa[2][NF], fb[2][FN];
     constexpr int NRB = NACT > 0 ? FN * FrB::PARTS : 0;
@@ -339,7 +373,7 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
         wait_lgkmcnt<(LEFT < 15 ? LEFT : 15)>();
         static_for<FN>([&](auto j_c) __attribute__((always_inline)) {
           constexpr int j = decltype(j_c)::value;
-          acc[i][j] = mfma_32x32x16<F16>(fb[BUFM][j], fa[BUFM][i], acc[i][j]);
+          acc[i][j] = group_mfma<EL>(fb[BUFM][j], fa[BUFM][i], acc[i][j]);
           if constexpr (!(SYNC && i == 0)) {
             constexpr int m = M0 + j;
             items(std::integral_constant<int, m * NIT / ND>{},
@@ -451,7 +485,8 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
         for (int q = 0; q < 4; ++q) {
           f32x4 w;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = acc[i][j][4 * q + e];
+          for (int e = 0; e < 4; ++e)
+            w[e] = value(i_c, std::integral_constant<int, j>{}, 4 * q + e);
           const int c = decltype(jj_c)::value * 8 + q * 2 + half;
           *(lds_u32x4_rw *)(uintptr_t)(stage + r32 * SROW + ((c ^ (r32 % CH)) * 16)) =
               __builtin_bit_cast(u32x4, w);
@@ -512,7 +547,7 @@ __device__ __forceinline__ bool run_group_tile(const GroupTile &t, char *smem, b
           uint32_t d[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            d[e] = pack_half<F16>(acc[i][j][8 * q + 2 * e], acc[i][j][8 * q + 2 * e + 1]);
+            d[e] = pack_half<F16>(value(i_c, j_c, 8 * q + 2 * e), value(i_c, j_c, 8 * q + 2 * e + 1));
           // lanes l and l ^ 32 trade halves: eight columns a lane
           swap_halves(d[0], d[2]);
           swap_halves(d[1], d[3]);

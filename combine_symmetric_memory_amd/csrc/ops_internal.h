@@ -51,6 +51,9 @@ struct GroupArgs {
   int32_t accumulate;     // dw: add to C
   int32_t parts;          // parts of the reduction, whose sums go to ws: 1 unsplit
   float *ws;              // [parts][rows of C][columns of C]
+  // 8-bit product only: A and B int8, C = sums * rs of the row * cs of the column
+  const float *rs, *cs;   // [rows] at distance ldrs, [groups][n]
+  int64_t ldrs;
 };
 enum GroupOp { kGroupProduct = 0, kGroupDx = 1, kGroupDw = 2 };
 // Parts a product of whole 16-byte rows is split into when it has workspace.
@@ -61,6 +64,38 @@ hipError_t launch_group_dw(bool f16, bool out_f32, bool aligned, const GroupArgs
                            hipStream_t st);
 hipError_t launch_group(GroupOp op, bool f16, bool out_f32, bool aligned, const GroupArgs &a,
                         hipStream_t st);
+
+// The 8-bit product; aligned: k and lda count pairs of elements (whole
+// 16-byte rows as the 16-bit kernels see them), otherwise elements.
+hipError_t launch_group_i8(int out_dtype, bool aligned, const GroupArgs &a, hipStream_t st);
+
+// ------------------------------------------------------- rows to 8 bits
+struct QuantArgs {
+  const void *x;
+  int64_t ldx;
+  int32_t rows, cols;  // of q
+  int8_t *q;
+  int64_t ldq;
+  float *s;
+  int64_t lds;
+};
+hipError_t launch_quant(int dtype, bool swiglu, const QuantArgs &a, hipStream_t st);
+
+// --------------------------------------------- the layer for a few tokens
+constexpr int kFewMaxTokens = 64;
+struct FewArgs {
+  int32_t T, K, E, H, I;
+  int32_t Ipad;           // row distance of h
+  int64_t plane;          // elements from h's high part to its low part
+  const int32_t *idx;     // [T][K]
+  const float *w;         // [T][K]
+  const char *x;          // [T][H]
+  const char *w13, *w2;   // [E][2 I][H], [E][H][I]
+  const float *s13, *s2;  // 8-bit weights: [E][2 I], [E][H]
+  uint16_t *h;            // [2][T K][Ipad]
+  void *out;              // [T][H]
+};
+hipError_t launch_moe_few(bool f16, bool i8, const FewArgs &a, hipStream_t st);
 
 // -------------------------------------------------------------- the norms
 struct NormArgs {

@@ -1,11 +1,16 @@
 """Python binding of the operators around the MoE path (include/cco_ops.h):
-the router, the products grouped by expert and the norms around a block.
+the router, the products grouped by expert, in 16 and in 8 bits, the layer for
+a few tokens and the norms around a block.
 
     idx, w = route(logits, topk, ...)                    # cco_route
     dlogits = route_grad(logits, idx, dw, ...)           # cco_route_grad
     y  = group_product(first, count, x, w)               # cco_group_product
     dx = group_product_dx(first, count, dy, w)           # cco_group_product_dx
     dw = group_product_dw(first, count, dy, x)           # cco_group_product_dw
+    q, s = quant_rows(x)                                 # cco_quant_rows
+    q, s = quant_swiglu(gate_up)                         # cco_quant_rows, swiglu
+    y  = group_product_i8(first, count, q, s, wq, ws)    # cco_group_product_i8
+    out = moe_few(x, idx, w, w13, w2, s13=, s2=)         # cco_moe_few
     out, u = block_norm(x, y, post=, gate=, pre=)        # cco_block_norm
     dx, dy, dpost, dgate, dpre = block_norm_grad(...)    # cco_block_norm_grad
     out, u, y = combine_norm(moe, x, w, post=, ...)      # cco_moe_combine_norm
@@ -303,6 +308,143 @@ def group_product_dw(first: torch.Tensor, count: torch.Tensor, dy: torch.Tensor,
                                    ldx, n, k, out.data_ptr(), _dtype(out, "out"),
                                    int(bool(accumulate)), _p(ws), nbytes,
                                    _raw_stream(dev.index)), "cco_group_product_dw")
+    return out
+
+
+# ------------------------------------------------------------- in 8 bits --
+def _distance(t: torch.Tensor, dev, name: str, rows: int) -> int:
+    """An fp32 [rows] vector; returns the distance of its elements."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError("%s must be a tensor on %s" % (name, dev))
+    if t.shape != (rows,) or t.dtype != torch.float32:
+        raise ValueError("%s must be float32 [%d], got %s %s" % (name, rows, t.dtype,
+                                                                tuple(t.shape)))
+    if rows <= 1:
+        return 1
+    if t.stride(0) < 1:
+        raise ValueError("the elements of %s overlap" % name)
+    return t.stride(0)
+
+
+def _quant(x, halves, out, scales, stream, name):
+    dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return _quant(x, halves, out, scales, None, name)
+    ldx = _rows(x, dev, "x")
+    code = _dtype(x, "x")
+    rows, cols = x.shape
+    if cols % halves:
+        raise ValueError("x must have the gate's and as many up columns, got %d" % cols)
+    cols //= halves
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    ldq = _rows(out, dev, "out", cols, rows, torch.int8)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    lds = _distance(scales, dev, "scales", rows)
+    check(lib.cco_quant_rows(x.data_ptr(), code, ldx, rows, cols, int(halves == 2),
+                             out.data_ptr(), ldq, scales.data_ptr(), lds,
+                             _raw_stream(dev.index)), name)
+    return out, scales
+
+
+def quant_rows(x: torch.Tensor, *, out: torch.Tensor | None = None,
+               scales: torch.Tensor | None = None, stream=None):
+    """cco_quant_rows -> (q int8 [rows, cols], s fp32 [rows]): q s is x to half
+    a step of s, the row's largest magnitude at 127.  x [rows, cols] bf16, fp16
+    or fp32 with contiguous rows; scales may have any distance."""
+    return _quant(x, 1, out, scales, stream, "quant_rows")
+
+
+def quant_swiglu(x: torch.Tensor, *, out: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, stream=None):
+    """cco_quant_rows with swiglu -> (q int8 [rows, inter], s fp32 [rows]) of
+    silu(gate) * up, the rows of the down product.  x [rows, 2 inter]: the
+    gate's columns, then the up columns."""
+    return _quant(x, 2, out, scales, stream, "quant_swiglu")
+
+
+def group_product_i8(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, xs: torch.Tensor,
+                     w: torch.Tensor, ws: torch.Tensor, *, out: torch.Tensor | None = None,
+                     dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """cco_group_product_i8: y [rows, n], y[r] = xs[r] ws[g] (x[r] w[g]^T) for
+    the rows r of every group g.  x int8 [rows, k] with contiguous rows, xs
+    fp32 [rows], w int8 [groups, n, k], ws fp32 [groups, n].  The result is
+    `out`'s type, or `dtype` (bf16, fp16 or fp32; bf16 if neither is given);
+    rows of no group keep what `out` holds."""
+    dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return group_product_i8(first, count, x, xs, w, ws, out=out, dtype=dtype)
+    ldx = _rows(x, dev, "x", None, None, torch.int8)
+    rows, k = x.shape
+    ldxs = _distance(xs, dev, "xs", rows)
+    g = _groups(first, count, rows, dev)
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [groups, n, k]")
+    n = w.shape[1]
+    _counts("w", n)
+    _same(w, dev, "w", (g.groups, n, k), torch.int8)
+    _same(ws, dev, "ws", (g.groups, n), torch.float32)
+    if out is None:
+        out = torch.empty((rows, n), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    ldy = _rows(out, dev, "out", n, rows, dtype)
+    code = _dtype(out, "out")
+    nbytes = lib.cco_group_product_i8_workspace(ctypes.byref(g), n, k)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    check(lib.cco_group_product_i8(ctypes.byref(g), x.data_ptr(), ldx, xs.data_ptr(), ldxs,
+                                   w.data_ptr(), ws.data_ptr(), n, k, out.data_ptr(), code, ldy,
+                                   _p(scratch), nbytes, _raw_stream(dev.index)),
+          "cco_group_product_i8")
+    return out
+
+
+# ------------------------------------------------ the layer for a few tokens --
+def moe_few(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, w13: torch.Tensor,
+            w2: torch.Tensor, *, s13: torch.Tensor | None = None, s2: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """cco_moe_few: the whole layer for at most 64 tokens in two launches, what
+    MoE.plan, dispatch, expert and combine give (only the result is rounded).
+    x [T, H] bf16 or fp16; idx int32 and w fp32 [T, K], as route gives them
+    (ids outside the experts take no part); w13 [E, 2 I, H] and w2 [E, H, I] of
+    x's type, or int8 with the scales s13 fp32 [E, 2 I] and s2 fp32 [E, H]."""
+    dev = _device(x, "x")
+    if _away(dev, stream):
+        with _Elsewhere(dev, stream):
+            return moe_few(x, idx, w, w13, w2, s13=s13, s2=s2, out=out)
+    code = _dtype(x, "x", _HALF)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    _same(x, dev, "x")
+    T, H = x.shape
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2:
+        raise ValueError("idx must be [T, K]")
+    K = idx.shape[1]
+    _same(idx, dev, "idx", (T, K), torch.int32)
+    _same(w, dev, "w", (T, K), torch.float32)
+    if not isinstance(w2, torch.Tensor) or w2.dim() != 3:
+        raise ValueError("w2 must be [E, H, I]")
+    E, I = w2.shape[0], w2.shape[2]
+    _counts("x, idx and w2", T, H, K, E, I)
+    i8 = w2.dtype == torch.int8
+    wtype = torch.int8 if i8 else x.dtype
+    _same(w13, dev, "w13", (E, 2 * I, H), wtype)
+    _same(w2, dev, "w2", (E, H, I), wtype)
+    if i8 != (s13 is not None) or i8 != (s2 is not None):
+        raise ValueError("s13 and s2 belong to int8 weights")
+    _same(s13, dev, "s13", (E, 2 * I), torch.float32)
+    _same(s2, dev, "s2", (E, H), torch.float32)
+    if out is None:
+        out = torch.empty_like(x)
+    _same(out, dev, "out", x.shape, x.dtype)
+    d = _capi.cco_few_desc(H, I, E, K, code, _capi.CCO_I8 if i8 else code, w13.data_ptr(),
+                           w2.data_ptr(), _p(s13), _p(s2))
+    nbytes = lib.cco_moe_few_workspace(ctypes.byref(d), T)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    check(lib.cco_moe_few(ctypes.byref(d), x.data_ptr(), idx.data_ptr(), w.data_ptr(), T,
+                          out.data_ptr(), _p(scratch), nbytes, _raw_stream(dev.index)),
+          "cco_moe_few")
     return out
 
 

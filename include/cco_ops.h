@@ -1,7 +1,9 @@
 /*
  * cco_ops.h -- operators around the MoE path of cco_moe.h, one MI355X
  * (gfx950): the router, the products grouped by expert with their
- * gradients, and the norms around a block fused with its gate and residual.
+ * gradients, in 16 bits or in 8-bit integers, the rows they take in 8 bits,
+ * a whole layer for a few tokens, and the norms around a block fused with its
+ * gate and residual.
  *
  * Conventions are those of cco_moe.h: every call returns a cco_status,
  * argument errors are reported before anything is launched, launches are
@@ -29,8 +31,8 @@
 extern "C" {
 #endif
 
-/* Element types. */
-typedef enum { CCO_BF16 = 0, CCO_F16 = 1, CCO_F32 = 2 } cco_dtype;
+/* Element types (CCO_I8: signed 8-bit integers, where stated). */
+typedef enum { CCO_BF16 = 0, CCO_F16 = 1, CCO_F32 = 2, CCO_I8 = 3 } cco_dtype;
 
 /* -------------------------------------------------------- the router --- */
 
@@ -137,6 +139,85 @@ int cco_group_product_dw(const cco_groups *g, int32_t dtype, const void *dy, int
                          const void *x, int64_t ldx, int32_t n, int32_t k, void *dw,
                          int32_t out_dtype, int32_t accumulate, void *workspace,
                          uint64_t workspace_bytes, void *stream);
+
+/* -------------------------------------------------- rows in 8 bits ----- */
+
+/* Rows to signed 8-bit integers with one scale a row:
+ *   s[r]    = max_c |v[r][c]| / 127
+ *   q[r][c] = 127 v[r][c] / max_c |v[r][c]|, rounded to nearest even as the
+ *             exact quotient is: between -127 and 127
+ * so q[r][c] * s[r] is v[r][c] to half a step of s[r].  A row of zeros gets
+ * zeros and s = 0; a row that holds a NaN or an infinity gets zeros and
+ * s = NaN, so that every product of it is NaN.
+ *   v      x[r][c], or with `swiglu` silu(x[r][c]) * x[r][cols + c] of rows
+ *          of 2 cols (gate, then up), in fp32
+ *   x      [rows] of `dtype` (bf16, fp16 or fp32), row distance ldx,
+ *          aligned to an element
+ *   q      device int8 [rows][cols], row distance ldq
+ *   s      device fp32, one a row at distance lds
+ * Columns and row distances lie in [1, 2^21).  The weights of
+ * cco_group_product_i8 are such rows too: [groups * n][k] gives w and ws. */
+int cco_quant_rows(const void *x, int32_t dtype, int64_t ldx, int32_t rows, int32_t cols,
+                   int32_t swiglu, int8_t *q, int64_t ldq, float *s, int64_t lds, void *stream);
+
+/* Bytes of workspace with which the 8-bit product of these sizes splits its
+ * reduction over workgroups (as cco_group_product_workspace). */
+uint64_t cco_group_product_i8_workspace(const cco_groups *g, int32_t n, int32_t k);
+
+/* y[r][n] = xs[r] * ws[g][n] * sum_k x[r][k] * w[g][n][k] for the rows r of
+ * every group g.  The sums are exact (int32): each is rounded to fp32, times
+ * xs, times ws, and rounded to y's type.  Split or not, the results are the
+ * same.
+ *   x      device int8 [rows][k], row distance ldx
+ *   xs     device fp32, one a row at distance ldxs: rows as
+ *          cco_moe_dispatch_fp8 leaves them in a receive window (the row's
+ *          bytes, then its scale) fit in place
+ *   w      device int8 [groups][n][k], dense;  ws  device fp32 [groups][n]
+ *   y      [rows][n] of `out_dtype` (bf16, fp16 or fp32), row distance ldy
+ * n and the row distances lie in [1, 2^21), k in [1, 2^17), ldxs in
+ * [1, 2^40).
+ * Rows of whole 16 bytes (k and ldx multiples of 16, n and ldy of 8, pointers
+ * 16-byte aligned; xs to a float) take the fast kernel, others a general one.
+ *   workspace  as in cco_group_product */
+int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, const float *xs,
+                         int64_t ldxs, const int8_t *w, const float *ws, int32_t n, int32_t k,
+                         void *y, int32_t out_dtype, int64_t ldy, void *workspace,
+                         uint64_t workspace_bytes, void *stream);
+
+/* -------------------------------------------- the layer for a few tokens */
+
+/* A whole layer in two launches, for batches of at most 64 tokens: what
+ * plan, dispatch, expert and combine give, without a heap:
+ *   h      = silu(Wg_e x[t]) * (Wu_e x[t]),  e = idx[t][j]
+ *   out[t] = sum_j w[t][j] * W2_e h
+ * Ids may repeat in a token (each counts); a pair whose id lies outside
+ * [0, E) takes no part, and a token without any gets zeros.  The weights of
+ * experts that no token has are not read, and what a token gets does not
+ * depend on the others'.  Sums are fp32, h is held to 2^-17 of it, and only
+ * `out` is rounded. */
+typedef struct {
+  int32_t hidden;      /* H, 1 .. 2^20 */
+  int32_t inter;       /* I, 1 .. 2^20 */
+  int32_t num_experts; /* E, 1..1024 */
+  int32_t topk;        /* K, 1..32 */
+  int32_t dtype;       /* x and out: CCO_BF16 or CCO_F16 */
+  int32_t wdtype;      /* w13 and w2: dtype, or CCO_I8 */
+  const void *w13;     /* [E][2 I][H]: the gate's rows, then the up rows */
+  const void *w2;      /* [E][H][I] */
+  const float *s13;    /* CCO_I8: scales [E][2 I]; otherwise NULL */
+  const float *s2;     /* CCO_I8: scales [E][H]; otherwise NULL */
+} cco_few_desc;
+
+/* Bytes of workspace for T tokens (0: none, or invalid). */
+uint64_t cco_moe_few_workspace(const cco_few_desc *d, int32_t T);
+
+/* x, out  device [T][H], dense;  idx device int32 [T][K];  w device fp32
+ *         [T][K];  all aligned to an element, the weights too
+ * workspace  device, 16-byte aligned, of the size above, in use until the
+ *         call's kernels have run
+ * More than 64 tokens: CCO_ERR_TOO_LARGE. */
+int cco_moe_few(const cco_few_desc *d, const void *x, const int32_t *idx, const float *w,
+                int32_t T, void *out, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* --------------------------------------------- norms around a block ---- */
 
