@@ -94,6 +94,7 @@ struct FewArgs {
   const float *s13, *s2;  // 8-bit weights: [E][2 I], [E][H]
   uint16_t *h;            // [2][T K][Ipad]
   void *out;              // [T][H]
+  int32_t cols;           // output columns of a workgroup (set by the launch)
 };
 hipError_t launch_moe_few(bool f16, bool i8, const FewArgs &a, hipStream_t st);
 
