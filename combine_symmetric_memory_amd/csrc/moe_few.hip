@@ -1,5 +1,5 @@
-// moe_few.hip -- a whole mixture-of-experts layer for a few tokens in two
-// launches (include/cco_ops.h):
+// moe_few.hip -- a whole mixture-of-experts layer for a few tokens in two or
+// three launches (include/cco_ops.h):
 //
 //   h[t, e] = silu(Wg_e x[t]) * (Wu_e x[t])
 //   out[t]  = sum_e share[t][e] W2_e h[t, e]
@@ -20,148 +20,21 @@
 // weights of the second product are split the same way, exactly (fp16's
 // eleven bits into two bf16 values), so that h may exceed fp16's range.
 // 8-bit weights are exact in bf16 and fp16 and meet their scales in the sums.
-#include <type_traits>
-
-#include "group_common.h"
+//
+// What carries the stream is that a wavefront always has the next 8 KiB of
+// weights in flight, over the ends of tiles and experts too, with eight
+// wavefronts a CU that need 256 registers a lane for it: 16 wavefronts of 128
+// registers, which spill, took 1.25 to 1.4 times as long, chunks of 16 KiB 1.1
+// to 1.4 times.  One token of 256 experts of 7168 x 2048, top-8, bf16: gate
+// and up 5.9 TB/s, down 5.2; 16 tokens with 8-bit weights 6.8 TB/s in all.
+#include "few_common.h"
 
 namespace cco {
 namespace {
 
-constexpr int kFewRows = 16;       // weight rows of an MFMA
-constexpr int kFewStepBytes = 64;  // bytes of a weight row a step takes
-
-__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ u32x4 load16(const char *p) {
-  u32x4 v;
-  __builtin_memcpy(&v, p, 16);
-  return v;
-}
-// 16 bytes at p, of which the first `have` exist; the others are zeros.
-__device__ __forceinline__ u32x4 load16(const char *p, int have) {
-  if (have >= 16) return load16(p);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < have) v[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
-  return v;
-}
-
 // Tiles of 16 tokens multiplied at once.  (With four the 8-bit forms spill; an
 // expert of more than 32 tokens has its weights read again, from the caches.)
 constexpr int kFewColumns = 2;
-
-// The ids and weights of a call in LDS, and the experts in use.
-struct FewIds {
-  uint32_t live[kMaxExperts / 32];
-  int32_t ids[kFewMaxTokens * kMaxTopk];
-  float w[kFewMaxTokens * kMaxTopk];
-};
-
-template <int THREADS>
-__device__ __forceinline__ void few_read_ids(const FewArgs &a, FewIds &s) {
-  for (int i = threadIdx.x; i < kMaxExperts / 32; i += THREADS) s.live[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * a.K; i += THREADS) {
-    const int e = a.idx[i];
-    s.ids[i] = e;
-    s.w[i] = a.w[i];
-    if (e >= 0 && e < a.E) atomicOr(&s.live[e / 32], 1u << (e % 32));
-  }
-  __syncthreads();
-}
-
-// The experts in use, in ascending order: how many, and the one of rank a.
-struct FewExperts {
-  int count;
-  int before;  // lane l: experts in use below 32 l
-  uint32_t word;
-  __device__ __forceinline__ explicit FewExperts(const FewIds &s) {
-    const int lane = threadIdx.x % kWave;
-    word = lane < kMaxExperts / 32 ? s.live[lane] : 0u;
-    const int n = __popc(word);
-    int incl = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up(incl, d, kWave);
-      if (lane >= d) incl += up;
-    }
-    before = incl - n;
-    count = uniform(__shfl(incl, kMaxExperts / 32 - 1, kWave));
-  }
-  __device__ __forceinline__ int at(int rank) const {
-    const int lane = threadIdx.x % kWave;
-    const uint64_t hit = __ballot(rank >= before && rank < before + __popc(word));
-    const int l = __builtin_ctzll(hit);
-    uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)word, l);
-    for (int k = rank - __builtin_amdgcn_readlane(before, l); k > 0; --k) w &= w - 1;
-    return uniform(l * 32 + __builtin_ctz(w));
-  }
-};
-
-// An expert's tokens, in ascending order.
-struct FewTokens {
-  int count;
-  int pair;  // lane n < count: first pair (token * K + j) of the n-th token ..
-  float share;  // .. and the sum of its weights for the expert
-  __device__ __forceinline__ void find(const FewArgs &a, const FewIds &s, int e) {
-    const int lane = threadIdx.x % kWave;
-    int first = -1;
-    float sum = 0.0f;
-    if (lane < a.T)
-      for (int j = a.K - 1; j >= 0; --j)
-        if (s.ids[lane * a.K + j] == e) first = lane * a.K + j;
-    if (first >= 0)
-      for (int p = first; p < (lane + 1) * a.K; ++p)
-        if (s.ids[p] == e) sum = p == first ? s.w[p] : sum + s.w[p];
-    const uint64_t mask = __ballot(first >= 0), below = (1ull << lane) - 1;
-    count = uniform(__popcll(mask));
-    // lane t's values go to the lane of its rank, other lanes' behind them
-    const int to = first >= 0 ? __popcll(mask & below) : count + __popcll(~mask & below);
-    pair = __builtin_amdgcn_ds_permute(to * 4, first);
-    share = __builtin_bit_cast(
-        float, __builtin_amdgcn_ds_permute(to * 4, __builtin_bit_cast(int, sum)));
-  }
-};
-
-// Two bf16 halves of the top 16 bits of a and b.
-__device__ __forceinline__ uint32_t top_halves(float a, float b) {
-  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a),
-                               0x07060302u);
-}
-// Eight 8-bit integers as bf16 or fp16 values, exact in both.
-template <bool F16>
-__device__ __forceinline__ u32x4 from_i8(uint32_t lo, uint32_t hi) {
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? lo : hi;
-    const int sh = 16 * (i % 2);
-    const float a = (float)(int8_t)(w >> sh), b = (float)(int8_t)(w >> (sh + 8));
-    if constexpr (F16)
-      r[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
-    else
-      r[i] = top_halves(a, b);
-  }
-  return r;
-}
-// Eight fp16 values as the sum of two bf16 ones.
-__device__ __forceinline__ void split_f16(u32x4 v, u32x4 &hi, u32x4 &lo) {
-  const f16x8 h = __builtin_bit_cast(f16x8, v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = (float)h[2 * i], b = (float)h[2 * i + 1];
-    hi[i] = top_halves(a, b);
-    const float ah = __builtin_bit_cast(float, hi[i] << 16);
-    const float bh = __builtin_bit_cast(float, hi[i] & 0xffff0000u);
-    lo[i] = top_halves(a - ah, b - bh);
-  }
-}
 
 // The product of MT tiles of weight rows with the columns of an expert's
 // tokens.  EL: the weights' elements.  PAIR: the columns are h, in two planes;
@@ -184,13 +57,12 @@ struct FewStream {
     u32x4 v[U][MT];
   };
   struct Tiles {
-    const char *a[MT];  // uniform: first rows of the tiles
+    GlobalBytes *a[MT];  // uniform: first rows of the tiles
   };
   uint32_t arow[MT];  // this lane's row in the tiles and its piece of a step, in bytes
   int piece;          // which 16 bytes of a step are this lane's
   int abytes;         // bytes of a weight row
-  const char *b;      // uniform: x, or the high plane of h
-  uint64_t plane;     // bytes between the planes of h
+  GlobalBytes *b;     // uniform: x, or h
   int bbytes;         // bytes of a column that may be read
 
   // Chunks of a row, the last one's end included, and those that are whole.
@@ -223,14 +95,14 @@ struct FewStream {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < NB; ++h)
-            col[u][n][h] = load16(b + (h / HALVES) * plane + (brow[n] + s) +
+            col[u][n][h] = load16(b + (h / HALVES) * bbytes + (brow[n] + s) +
                                   (u * kFewStepBytes * HALVES + (h % HALVES) * 16));
       if (u0 + G >= U && ahead) load_rows(next, nt, nc);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < G; ++u)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) multiply<NT>(acc[i], now.v[u0 + u][i], col[u]);
+        for (int i = 0; i < MT; ++i) few_multiply<EL, PAIR, XF16, NT, NB>(acc[i], now.v[u0 + u][i], col[u]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -248,49 +120,11 @@ struct FewStream {
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
         const int in = (h % HALVES) * 16;
-        col[n][h] = load16(b + (h / HALVES) * plane + brow[n] + s * kFewStepBytes * HALVES + in,
+        col[n][h] = load16(b + (h / HALVES) * bbytes + brow[n] + s * kFewStepBytes * HALVES + in,
                            bbytes - at * HALVES - in);
       }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) multiply<NT>(acc[i], w[i], col);
-  }
-  template <int NT>
-  static __device__ __forceinline__ void multiply(f32x4 (&acc)[NT], u32x4 w,
-                                                  const u32x4 (&col)[NT][NB]) {
-    constexpr bool F = XF16 && !PAIR;
-    using V = std::conditional_t<F, f16x8, bf16x8>;
-    auto mma = [&](int n, u32x4 x, u32x4 y) __attribute__((always_inline)) {
-      acc[n] = mfma16(__builtin_bit_cast(V, x), __builtin_bit_cast(V, y), acc[n]);
-    };
-    // Weights are converted where they are multiplied.  (Left to itself the
-    // compiler takes the loaded vectors apart into bytes and converts them all
-    // ahead, which spills.)
-    if constexpr (EL == kElemI8 || (EL == kElemF16 && PAIR)) asm volatile("" : "+v"(w));
-    if constexpr (EL == kElemI8) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 f = from_i8<F>(w[2 * h], w[2 * h + 1]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int p = 0; p < (PAIR ? 2 : 1); ++p) mma(n, f, col[n][p * 2 + h]);
-      }
-    } else if constexpr (EL == kElemF16 && PAIR) {
-      u32x4 hi, lo;
-      split_f16(w, hi, lo);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        // (the product of the two low parts is 2^-16 of the whole)
-        mma(n, hi, col[n][0]);
-        mma(n, hi, col[n][1]);
-        mma(n, lo, col[n][0]);
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int p = 0; p < NB; ++p) mma(n, w, col[n][p]);
-    }
+    for (int i = 0; i < MT; ++i) few_multiply<EL, PAIR, XF16, NT, NB>(acc[i], w[i], col);
   }
   // Chunks [from, to) of tiles t.  The rows of a range's first whole chunk are
   // in flight into r0 when it begins; with `more` those of chunk nc of tiles
@@ -343,7 +177,7 @@ struct FewUp {
     typename Stream::Tiles t;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      t.a[i] = uniform(a.w13 + (((int64_t)e * 2 + i) * a.I + first_row(a, it)) * (a.H * ES));
+      t.a[i] = uniform_bytes(a.w13 + (((int64_t)e * 2 + i) * a.I + first_row(a, it)) * (a.H * ES));
     return t;
   }
   // The last tile lies back so that it is whole (its first rows are computed
@@ -403,25 +237,22 @@ struct FewUp {
           }
           h = silu(gv) * uv;
         }
-        hi[v] = f32_to_bf16_rne(h);
-        const float left = h - from_half_bits<false>(hi[v]);
-        // (an infinite or NaN h is whole in its high part)
-        lo[v] = left == left ? f32_to_bf16_rne(left) : 0;
+        few_split(h, hi[v], lo[v]);
       }
       if (want < tk.count) {
-        uint16_t *row = a.h + (int64_t)pair * a.Ipad;
+        uint16_t *row = a.h + (int64_t)pair * 2 * a.Ipad;
         if (i0 + 4 <= a.I) {
           __builtin_memcpy(row + i0, hi, 8);
-          __builtin_memcpy(row + a.plane + i0, lo, 8);
+          __builtin_memcpy(row + a.Ipad + i0, lo, 8);
         } else {
           for (int v = 0; v < a.I - i0; ++v) {
             row[i0 + v] = hi[v];
-            row[a.plane + i0 + v] = lo[v];
+            row[a.Ipad + i0 + v] = lo[v];
           }
         }
         // the padding behind the last tile
         if ((it + 1) * kFewRows >= a.I)
-          for (int c = a.I + piece; c < a.Ipad; c += 4) row[c] = row[a.plane + c] = 0;
+          for (int c = a.I + piece; c < a.Ipad; c += 4) row[c] = row[a.Ipad + c] = 0;
       }
     }
   }
@@ -429,8 +260,9 @@ struct FewUp {
 
 template <GroupElem EL, bool XF16>
 __global__ __launch_bounds__(kUpThreads, 2) void few_up_kernel(FewArgs a) {
-  __shared__ FewIds s;
+  __shared__ uint32_t id_words[FewIds::words(kFewMaxTokens * kMaxTopk)];
   __shared__ UpSums sums;
+  const FewIds s(id_words, a.T * a.K);
   using Up = FewUp<EL, XF16>;
   using Stream = typename Up::Stream;
   few_read_ids<kUpThreads>(a, s);
@@ -440,8 +272,7 @@ __global__ __launch_bounds__(kUpThreads, 2) void few_up_kernel(FewArgs a) {
   Stream st;
   st.abytes = a.H * Up::ES;
   st.bbytes = a.H * 2;
-  st.b = a.x;
-  st.plane = 0;
+  st.b = (GlobalBytes *)a.x;
   st.piece = lane / 16;
   st.arow[0] = st.arow[1] =
       (uint32_t)min(lane % 16, a.I - 1) * (uint32_t)st.abytes + st.piece * 16;
@@ -493,7 +324,7 @@ struct FewDown {
                                                                     int n0) {
     typename Stream::Tiles t;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) t.a[i] = uniform(a.w2 + ((int64_t)e * a.H + n0) * (a.I * ES));
+    for (int i = 0; i < MT; ++i) t.a[i] = uniform_bytes(a.w2 + ((int64_t)e * a.H + n0) * (a.I * ES));
     return t;
   }
 
@@ -518,7 +349,7 @@ struct FewDown {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int want = base + n * 16 + col;
-      brow[n] = (uint32_t)__shfl(tk.pair, want < tk.count ? want : base, kWave) * st.bbytes +
+      brow[n] = (uint32_t)__shfl(tk.pair, want < tk.count ? want : base, kWave) * 2 * st.bbytes +
                 piece * 16 * st.HALVES;
 #pragma unroll
       for (int i = 0; i < MT; ++i) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -545,7 +376,8 @@ __global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_
   using Down = FewDown<EL, MT>;
   using Stream = typename Down::Stream;
   constexpr int SUMS = Down::SUMS;
-  __shared__ FewIds s;
+  __shared__ uint32_t id_words[FewIds::words(kFewMaxTokens * kMaxTopk)];
+  const FewIds s(id_words, a.T * a.K);
   extern __shared__ __align__(16) float sums[];  // [WAVES][T][SUMS]
   const int wave = uniform((int)threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int n0 = blockIdx.x * a.cols;
@@ -556,8 +388,7 @@ __global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_
   Stream st;
   st.abytes = a.I * Down::ES;
   st.bbytes = a.Ipad * 2;
-  st.b = (const char *)a.h;
-  st.plane = a.plane * 2;
+  st.b = (GlobalBytes *)a.h;
   st.piece = lane / 16;
   // rows past the workgroup's last repeat it
 #pragma unroll
@@ -626,6 +457,7 @@ hipError_t launch_few(FewArgs a, hipStream_t st) {
   hipLaunchKernelGGL((few_up_kernel<EL, XF16>), dim3((uint32_t)grid), dim3(kUpThreads), 0, st, a);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
+  if (a.parts > 0) return launch_few_shared(XF16, EL == kElemI8, a, st);
   // one workgroup on every CU, or whole rounds of them
   const int rounds = (a.H + 32 * kNumCus - 1) / (32 * kNumCus);
   a.cols = std::max(kFewRows, (a.H + rounds * kNumCus - 1) / (rounds * kNumCus));

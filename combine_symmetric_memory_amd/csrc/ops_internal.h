@@ -85,17 +85,22 @@ hipError_t launch_quant(int dtype, bool swiglu, const QuantArgs &a, hipStream_t 
 constexpr int kFewMaxTokens = 64;
 struct FewArgs {
   int32_t T, K, E, H, I;
-  int32_t Ipad;           // row distance of h
-  int64_t plane;          // elements from h's high part to its low part
+  int32_t Ipad;           // row distance of h's planes
   const int32_t *idx;     // [T][K]
   const float *w;         // [T][K]
   const char *x;          // [T][H]
   const char *w13, *w2;   // [E][2 I][H], [E][H][I]
   const float *s13, *s2;  // 8-bit weights: [E][2 I], [E][H]
-  uint16_t *h;            // [2][T K][Ipad]
+  uint16_t *h;            // [T K][2][Ipad]: high parts, low parts
   void *out;              // [T][H]
   int32_t cols;           // output columns of a workgroup (set by the launch)
+  // The down product's other form: parts of its reduction (0: that form is
+  // not taken) and, with several, their sums [parts][T][H].
+  int32_t parts;
+  float *partial;
 };
+int few_parts(bool i8, int32_t T, int32_t K, int32_t E, int32_t H, int32_t I);
+hipError_t launch_few_shared(bool f16, bool i8, const FewArgs &a, hipStream_t st);
 hipError_t launch_moe_few(bool f16, bool i8, const FewArgs &a, hipStream_t st);
 
 // -------------------------------------------------------------- the norms

@@ -23,15 +23,27 @@ bool groups_ok(const cco_groups *g) {
 }
 bool few_ok(const cco_few_desc *d, int32_t T) {
   if (!d || T < 0 || d->hidden < 1 || d->inter < 1 || d->hidden > (1 << 20) ||
-      d->inter > (1 << 20))
+      d->inter > (1 << 19))
     return false;
   if (d->num_experts < 1 || d->num_experts > cco::kMaxExperts) return false;
   if (d->topk < 1 || d->topk > cco::kMaxTopk) return false;
   if (d->dtype != CCO_BF16 && d->dtype != CCO_F16) return false;
   return d->wdtype == d->dtype || d->wdtype == CCO_I8;
 }
-// row distance of h: whole steps of the second product
-int32_t few_pitch(const cco_few_desc *d) { return (d->inter + 63) / 64 * 64; }
+// The workspace: h and the parts' sums.
+struct FewSpace {
+  int32_t pitch, parts;
+  uint64_t partial, bytes;  // where the sums begin, and the whole
+};
+FewSpace few_space(const cco_few_desc *d, int32_t T) {
+  FewSpace s{};
+  s.pitch = (d->inter + 255) / 256 * 256;  // whole chunks of the down product
+  s.parts = cco::few_parts(d->wdtype == CCO_I8, T, d->topk, d->num_experts, d->hidden, d->inter);
+  s.partial = (uint64_t)T * d->topk * 2 * s.pitch * sizeof(uint16_t);
+  s.bytes = s.partial +
+            (s.parts > 1 ? (uint64_t)s.parts * T * (uint64_t)d->hidden * sizeof(float) : 0);
+  return s;
+}
 
 }  // namespace
 
@@ -111,7 +123,7 @@ int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, cons
 
 uint64_t cco_moe_few_workspace(const cco_few_desc *d, int32_t T) {
   if (!few_ok(d, T) || T > cco::kFewMaxTokens) return 0;
-  return (uint64_t)2 * T * d->topk * few_pitch(d) * sizeof(uint16_t);
+  return T == 0 ? 0 : few_space(d, T).bytes;
 }
 
 int cco_moe_few(const cco_few_desc *d, const void *x, const int32_t *idx, const float *w,
@@ -135,8 +147,10 @@ int cco_moe_few(const cco_few_desc *d, const void *x, const int32_t *idx, const 
   a.E = d->num_experts;
   a.H = d->hidden;
   a.I = d->inter;
-  a.Ipad = few_pitch(d);
-  a.plane = (int64_t)T * d->topk * a.Ipad;
+  const FewSpace space = few_space(d, T);
+  a.Ipad = space.pitch;
+  a.parts = space.parts;
+  a.partial = (float *)((char *)workspace + space.partial);
   a.idx = idx;
   a.w = w;
   a.x = (const char *)x;

@@ -404,8 +404,8 @@ def group_product_i8(first: torch.Tensor, count: torch.Tensor, x: torch.Tensor, 
 def moe_few(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, w13: torch.Tensor,
             w2: torch.Tensor, *, s13: torch.Tensor | None = None, s2: torch.Tensor | None = None,
             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """cco_moe_few: the whole layer for at most 64 tokens in two launches, what
-    MoE.plan, dispatch, expert and combine give (only the result is rounded).
+    """cco_moe_few: the whole layer for at most 64 tokens in two or three
+    launches, what MoE.plan, dispatch, expert and combine give (only the result is rounded).
     x [T, H] bf16 or fp16; idx int32 and w fp32 [T, K], as route gives them
     (ids outside the experts take no part); w13 [E, 2 I, H] and w2 [E, H, I] of
     x's type, or int8 with the scales s13 fp32 [E, 2 I] and s2 fp32 [E, H]."""

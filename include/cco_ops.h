@@ -186,8 +186,8 @@ int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, cons
 
 /* -------------------------------------------- the layer for a few tokens */
 
-/* A whole layer in two launches, for batches of at most 64 tokens: what
- * plan, dispatch, expert and combine give, without a heap:
+/* A whole layer in two or three launches, for batches of at most 64 tokens:
+ * what plan, dispatch, expert and combine give, without a heap:
  *   h      = silu(Wg_e x[t]) * (Wu_e x[t]),  e = idx[t][j]
  *   out[t] = sum_j w[t][j] * W2_e h
  * Ids may repeat in a token (each counts); a pair whose id lies outside
@@ -197,7 +197,7 @@ int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, cons
  * `out` is rounded. */
 typedef struct {
   int32_t hidden;      /* H, 1 .. 2^20 */
-  int32_t inter;       /* I, 1 .. 2^20 */
+  int32_t inter;       /* I, 1 .. 2^19 */
   int32_t num_experts; /* E, 1..1024 */
   int32_t topk;        /* K, 1..32 */
   int32_t dtype;       /* x and out: CCO_BF16 or CCO_F16 */

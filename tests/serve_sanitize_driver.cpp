@@ -18,6 +18,7 @@ hipError_t launch_group_i8(int, bool, const GroupArgs &, hipStream_t) {
   return hipSuccess;
 }
 hipError_t launch_quant(int, bool, const QuantArgs &, hipStream_t) { ++launches; return hipSuccess; }
+int few_parts(bool, int32_t, int32_t, int32_t, int32_t H, int32_t) { return H > 16 ? 32 : 0; }
 hipError_t launch_moe_few(bool, bool, const FewArgs &, hipStream_t) {
   ++launches;
   return hipSuccess;
@@ -69,7 +70,7 @@ int main() {
           cco_few_desc d{H, I, 8, K, CCO_BF16, CCO_I8, p, p, f, f};
           const uint64_t ws = cco_moe_few_workspace(&d, T);
           const int rc = cco_moe_few(&d, p, i, f, T, p, p, ws, nullptr);
-          const bool ok = H >= 1 && H <= (1 << 20) && I >= 1 && I <= (1 << 20) && K >= 1 &&
+          const bool ok = H >= 1 && H <= (1 << 20) && I >= 1 && I <= (1 << 19) && K >= 1 &&
                           K <= 32 && T >= 0;
           CHECK(rc == (!ok ? CCO_ERR_INVALID_ARG : T > 64 ? CCO_ERR_TOO_LARGE : CCO_OK));
           CHECK((ws > 0) == (ok && T > 0 && T <= 64));

@@ -72,6 +72,16 @@ def test_odd_sizes(cco, dtype, wdtype, H, I):
         _check(cco, _case(T, H, I, 6, 3, dtype, wdtype, H))
 
 
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+@pytest.mark.parametrize("T,H,I,E,K", [(20, 200, 1003, 3, 2), (40, 130, 2048, 2, 1),
+                                       (9, 16, 8, 2, 2), (3, 4100, 700, 1, 1),
+                                       (1, 4112, 300, 2, 1), (64, 80, 257, 4, 4)])
+def test_both_forms_of_the_down_product(cco, dtype, wdtype, T, H, I, E, K):
+    # several parts of the reduction, ends of rows and of column blocks
+    say("case: few down %s %s T=%d H=%d I=%d E=%d K=%d" % (dtype, wdtype, T, H, I, E, K))
+    _check(cco, _case(T, H, I, E, K, dtype, wdtype, T + I))
+
+
 @pytest.mark.parametrize("wdtype", [BF, torch.int8])
 def test_pairs_that_take_no_part(cco, wdtype):
     c = _case(12, 128, 96, 7, 3, BF, wdtype, 1)

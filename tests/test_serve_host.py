@@ -79,7 +79,7 @@ def _few(capi, H=64, I=32, E=4, K=2, dtype=0, wdtype=0, w13=P, w2=P, s13=None, s
     return ctypes.byref(capi.cco_few_desc(H, I, E, K, dtype, wdtype, w13, w2, s13, s2))
 
 
-@pytest.mark.parametrize("kw", [dict(H=0), dict(I=0), dict(H=(1 << 20) + 1), dict(I=(1 << 20) + 1),
+@pytest.mark.parametrize("kw", [dict(H=0), dict(I=0), dict(H=(1 << 20) + 1), dict(I=(1 << 19) + 1),
                                 dict(E=0), dict(E=1025), dict(K=0), dict(K=33), dict(dtype=2),
                                 dict(dtype=3, wdtype=3), dict(wdtype=1), dict(wdtype=2),
                                 dict(dtype=-1, wdtype=-1)])
@@ -93,7 +93,7 @@ def test_few_arguments(capi):
     F, W = capi.lib.cco_moe_few, capi.lib.cco_moe_few_workspace
     d = _few(capi)
     need = W(d, 4)
-    assert need == 2 * 4 * 2 * 64 * 2  # two planes of T K rows of I, whole steps
+    assert need == 4 * 2 * 2 * 256 * 2  # T K rows of two planes of I, whole chunks
     ok = [P, P, P, 4, P, P, need]
     for i, v in ((0, None), (0, P + 1), (1, None), (1, P + 2), (2, None), (2, P + 2), (3, -1),
                  (4, None), (4, P + 1), (5, None), (5, P + 8), (6, need - 1)):
