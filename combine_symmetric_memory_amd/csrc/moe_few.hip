@@ -44,15 +44,16 @@ constexpr int kFewColumns = 2;
 // The reduction goes by chunks of U steps.  The weights of the next chunk, be
 // it the same expert's or the next one's, are in flight while a chunk is
 // multiplied; its columns, which the caches hold, are issued before them and
-// waited for alone, UB steps at a time, so that they take few registers.  What
-// a row has behind its last whole chunk goes step by step.
+// waited for alone, UB steps at a time, so that they take few registers.
 template <GroupElem EL, bool PAIR, bool XF16, int MT>
 struct FewStream {
   static constexpr int HALVES = EL == kElemI8 ? 2 : 1;  // 16-byte pieces of a column a step
   static constexpr int NB = (PAIR ? 2 : 1) * HALVES;
   static constexpr int U = PAIR && EL == kElemI8 ? 4 : 8 / MT;
+  // pieces of columns in registers at once; conversions need some themselves
+  static constexpr int kColumnPieces = EL == kElemI8 ? 8 : 16;
   template <int NT>
-  static constexpr int UB = NT * NB >= 16 ? 1 : (16 / (NT * NB) < U ? 16 / (NT * NB) : U);
+  static constexpr int UB = kColumnPieces / (NT * NB) < U ? kColumnPieces / (NT * NB) : U;
   struct Rows {
     u32x4 v[U][MT];
   };
@@ -65,109 +66,133 @@ struct FewStream {
   GlobalBytes *b;     // uniform: x, or h
   int bbytes;         // bytes of a column that may be read
 
-  // Chunks of a row, the last one's end included, and those that are whole.
+  // Chunks of a row, the last one's end included.
   __device__ __forceinline__ int chunks() const {
     return (abytes + U * kFewStepBytes - 1) / (U * kFewStepBytes);
   }
-  __device__ __forceinline__ int whole() const { return abytes / (U * kFewStepBytes); }
+  // Whether rows end inside chunk c.
+  __device__ __forceinline__ bool ends(int c) const {
+    return (c + 1) * U * kFewStepBytes > abytes;
+  }
 
   __device__ __forceinline__ void load_rows(Rows &r, const Tiles &t, int c) const {
+    if (!ends(c)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          r.v[u][i] = load16(t.a[i] + (arow[i] + c * U * kFewStepBytes) + u * kFewStepBytes);
+      return;
+    }
+    // pieces that would pass the row's end take its last 16 bytes
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        r.v[u][i] = load16(t.a[i] + (arow[i] + c * U * kFewStepBytes) + u * kFewStepBytes);
+      for (int i = 0; i < MT; ++i) {
+        const int at = (c * U + u) * kFewStepBytes + piece * 16;
+        const uint32_t row = arow[i] - piece * 16;
+        r.v[u][i] = abytes >= 16 ? load16(t.a[i] + (row + (uint32_t)min(at, abytes - 16)))
+                                 : load16(t.a[i] + (row + min(at, abytes)), abytes - at);
+      }
+    // (keeps the compiler from one set of loads for both cases, at addresses
+    // of 64 bits each)
+    asm volatile("" ::: "memory");
   }
-  // acc += the product over the whole chunk c, whose rows are `now`; with
-  // `ahead` the rows of chunk nc of tiles nt are put in flight into `next`.
+  // What lies behind the row's end in its last chunk becomes zeros.
+  __device__ __forceinline__ void cut_rows(Rows &r, int c) const {
+    if (abytes < 16) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        r.v[u][i] = end_cut(r.v[u][i], (c * U + u) * kFewStepBytes + piece * 16, abytes);
+        asm volatile("" : "+v"(r.v[u][i]));  // one after the other, in few registers
+      }
+  }
+  // acc += the product over chunk c, whose rows are `now`; with `ahead` the
+  // rows of chunk nc of tiles nt are put in flight into `next`.
   template <int NT>
-  __device__ __forceinline__ void chunk(f32x4 (&acc)[MT][NT], const Rows &now, int c,
+  __device__ __forceinline__ void chunk(f32x4 (&acc)[MT][NT], Rows &now, int c,
                                         const uint32_t (&brow)[NT], Rows &next, bool ahead,
                                         const Tiles &nt, int nc) const {
     constexpr int G = UB<NT>;
+    const bool end = ends(c);
 #pragma unroll
     for (int u0 = 0; u0 < U; u0 += G) {
       u32x4 col[G][NT][NB];
       const int s = (c * U + u0) * kFewStepBytes * HALVES;
+      if (PAIR || !end) {
 #pragma unroll
-      for (int u = 0; u < G; ++u)
+        for (int u = 0; u < G; ++u)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int h = 0; h < NB; ++h)
-            col[u][n][h] = load16(b + (h / HALVES) * bbytes + (brow[n] + s) +
-                                  (u * kFewStepBytes * HALVES + (h % HALVES) * 16));
+            for (int h = 0; h < NB; ++h)
+              col[u][n][h] = load16(b + (h / HALVES) * bbytes + (brow[n] + s) +
+                                    (u * kFewStepBytes * HALVES + (h % HALVES) * 16));
+      } else {
+        // x ends with the row (h is padded with zeros to whole chunks)
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < NB; ++h) {
+              const int in = piece * 16 * HALVES;
+              const int at = s + u * kFewStepBytes * HALVES + in + h * 16;
+              const uint32_t row = brow[n] - in;
+              if (bbytes >= 16)
+                col[u][n][h] = end_cut(load16(b + (row + (uint32_t)min(at, bbytes - 16))), at, bbytes);
+              else
+                col[u][n][h] = load16(b + (row + min(at, bbytes)), bbytes - at);
+              asm volatile("" : "+v"(col[u][n][h]));
+            }
+      }
+      if (end && u0 == 0) cut_rows(now, c);
       if (u0 + G >= U && ahead) load_rows(next, nt, nc);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < G; ++u)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) few_multiply<EL, PAIR, XF16, NT, NB>(acc[i], now.v[u0 + u][i], col[u]);
+        for (int i = 0; i < MT; ++i)
+          few_multiply<EL, PAIR, XF16, NT, NB>(acc[i], now.v[u0 + u][i], col[u]);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // acc += the product over step s, in or behind which rows end.
-  template <int NT>
-  __device__ __forceinline__ void step(f32x4 (&acc)[MT][NT], const Tiles &t, int s,
-                                       const uint32_t (&brow)[NT]) const {
-    u32x4 col[NT][NB], w[MT];
-    const int at = s * kFewStepBytes + piece * 16;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      w[i] = load16(t.a[i] + arow[i] + s * kFewStepBytes, abytes - at);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        const int in = (h % HALVES) * 16;
-        col[n][h] = load16(b + (h / HALVES) * bbytes + brow[n] + s * kFewStepBytes * HALVES + in,
-                           bbytes - at * HALVES - in);
-      }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) few_multiply<EL, PAIR, XF16, NT, NB>(acc[i], w[i], col);
-  }
-  // Chunks [from, to) of tiles t.  The rows of a range's first whole chunk are
-  // in flight into r0 when it begins; with `more` those of chunk nc of tiles
-  // nt are when it ends (if that chunk is whole).
+  // Chunks [from, to) of tiles t.  The rows of the first are in flight into r0
+  // when the range begins; with `more` those of chunk nc of tiles nt are when
+  // it ends, into r0 again or, behind an odd number of chunks, into r1.
   template <int NT>
   __device__ __forceinline__ void run(f32x4 (&acc)[MT][NT], Rows &r0, Rows &r1, const Tiles &t,
                                       int from, int to, const uint32_t (&brow)[NT], bool more,
                                       const Tiles &nt, int nc) const {
-    const int in = min(to, whole());
-    more = more && nc < whole();
     int c = from;
 #pragma unroll 1
-    for (; c + 2 <= in; c += 2) {
+    for (; c + 2 <= to; c += 2) {
       chunk<NT>(acc, r0, c, brow, r1, true, t, c + 1);
-      const bool last = c + 2 >= in;
+      const bool last = c + 2 >= to;
       // the next range's where this one ends
       Tiles n;
 #pragma unroll
       for (int i = 0; i < MT; ++i) n.a[i] = last ? nt.a[i] : t.a[i];
       chunk<NT>(acc, r1, c + 1, brow, r0, !last || more, n, last ? nc : c + 2);
     }
-    if (c < in) chunk<NT>(acc, r0, c, brow, r1, false, t, c);
-    // (an even range's are on their way)
-    if ((c < in || from >= in) && more) load_rows(r0, nt, nc);
-    if (to > in) {
-      const int end = (abytes + kFewStepBytes - 1) / kFewStepBytes;
-#pragma unroll 1
-      for (int s = in * U; s < end; ++s) step<NT>(acc, t, s, brow);
-    }
+    if (c < to) chunk<NT>(acc, r0, c, brow, r1, more, nt, nc);
   }
 };
 
 // ---------------------------------------------------------- gate and up --
-// A workgroup takes tiles of 16 gate rows and their 16 up rows of an expert;
-// its wavefronts split the reduction and add their sums up in LDS, in order.
-// The sums of two tiles have room there, so one barrier a tile is enough: the
-// wavefront that adds a tile up does so while the others go on.
+// Tiles of 16 gate rows and their 16 up rows of an expert.  With PARTS a
+// workgroup's wavefronts split the reduction of a tile and add their sums up in
+// LDS, in order; the sums of two tiles have room there, so one barrier a tile
+// is enough: the wavefront that adds a tile up does so while the others go on.
+// Otherwise (PARTS 1) each wavefront takes tiles of its own.
 constexpr int kUpWaves = 4, kUpThreads = kUpWaves * kWave;
 struct UpSums {
   f32x4 v[2][kUpWaves][kFewColumns][2][kWave];
 };
 
-template <GroupElem EL, bool XF16>
+template <GroupElem EL, bool XF16, int PARTS>
 struct FewUp {
   using Stream = FewStream<EL, false, XF16, 2>;
   static constexpr int ES = EL == kElemI8 ? 1 : 2;
@@ -207,20 +232,26 @@ struct FewUp {
     }
     st.template run<NT>(acc, r0, r1, now, from, to, brow, more, nt, from);
     auto &red = sums.v[turn & 1];
+    if constexpr (PARTS > 1) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      red[wave][n][0][lane] = acc[0][n];
-      red[wave][n][1][lane] = acc[1][n];
+      for (int n = 0; n < NT; ++n) {
+        red[wave][n][0][lane] = acc[0][n];
+        red[wave][n][1][lane] = acc[1][n];
+      }
+      __syncthreads();
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int n = 0; n < NT; ++n) {
-      if ((turn + n) % kUpWaves != wave) continue;
-      f32x4 g = red[0][n][0][lane], u = red[0][n][1][lane];
 #pragma unroll
-      for (int w = 1; w < kUpWaves; ++w) {
-        g += red[w][n][0][lane];
-        u += red[w][n][1][lane];
+    for (int n = 0; n < NT; ++n) {
+      f32x4 g = acc[0][n], u = acc[1][n];
+      if constexpr (PARTS > 1) {
+        if ((turn + n) % PARTS != wave) continue;
+        g = red[0][n][0][lane];
+        u = red[0][n][1][lane];
+#pragma unroll
+        for (int w = 1; w < PARTS; ++w) {
+          g += red[w][n][0][lane];
+          u += red[w][n][1][lane];
+        }
       }
       // this lane: rows 4 piece .. of the tile, token `want`
       const int want = base + n * 16 + col, i0 = first_row(a, it) + piece * 4;
@@ -258,12 +289,12 @@ struct FewUp {
   }
 };
 
-template <GroupElem EL, bool XF16>
+template <GroupElem EL, bool XF16, int PARTS>
 __global__ __launch_bounds__(kUpThreads, 2) void few_up_kernel(FewArgs a) {
   __shared__ uint32_t id_words[FewIds::words(kFewMaxTokens * kMaxTopk)];
   __shared__ UpSums sums;
   const FewIds s(id_words, a.T * a.K);
-  using Up = FewUp<EL, XF16>;
+  using Up = FewUp<EL, XF16, PARTS>;
   using Stream = typename Up::Stream;
   few_read_ids<kUpThreads>(a, s);
   const FewExperts ex(s);
@@ -277,30 +308,44 @@ __global__ __launch_bounds__(kUpThreads, 2) void few_up_kernel(FewArgs a) {
   st.arow[0] = st.arow[1] =
       (uint32_t)min(lane % 16, a.I - 1) * (uint32_t)st.abytes + st.piece * 16;
   const int chunks = st.chunks();
-  const int from = chunks * wave / kUpWaves, to = chunks * (wave + 1) / kUpWaves;
-  int L = blockIdx.x;
+  const int from = PARTS > 1 ? chunks * wave / PARTS : 0;
+  const int to = PARTS > 1 ? chunks * (wave + 1) / PARTS : chunks;
+  int L = PARTS > 1 ? blockIdx.x : blockIdx.x * kUpWaves + wave;
+  const int step = PARTS > 1 ? gridDim.x : gridDim.x * kUpWaves;
   if (L >= all) return;
   int e = ex.at(L / tiles), it = L % tiles;
   typename Stream::Tiles now = Up::tiles_of(a, e, it);
   typename Stream::Rows r0, r1;
   int turn = 0;
-  if (from < min(to, st.whole())) st.load_rows(r0, now, from);
-  for (; L < all; L += gridDim.x) {
+  bool flip = false;
+  if (from < to) st.load_rows(r0, now, from);
+  for (; L < all; L += step) {
     FewTokens tk;
     tk.find(a, s, e);
-    const bool more = L + (int)gridDim.x < all;
-    const int ne = more ? ex.at((L + gridDim.x) / tiles) : e;
-    const int nit = more ? (L + gridDim.x) % tiles : it;
+    const bool more = L + step < all;
+    const int ne = more ? ex.at((L + step) / tiles) : e;
+    const int nit = more ? (L + step) % tiles : it;
     typename Stream::Tiles nt = Up::tiles_of(a, ne, nit);
     for (int base = 0; base < tk.count; base += 16 * kFewColumns) {
       const bool again = base + 16 * kFewColumns < tk.count;
       const typename Stream::Tiles then = again ? now : nt;
-      if (tk.count - base <= 16)
-        Up::template tile<1>(a, st, r0, r1, tk, e, it, base, now, from, to, more || again, then,
-                             sums, turn);
+      auto columns = [&](auto nt_c, typename Stream::Rows &x, typename Stream::Rows &y)
+                         __attribute__((always_inline)) {
+        Up::template tile<decltype(nt_c)::value>(a, st, x, y, tk, e, it, base, now, from, to,
+                                                 more || again, then, sums, turn);
+      };
+      auto tile = [&](typename Stream::Rows &x, typename Stream::Rows &y)
+                      __attribute__((always_inline)) {
+        if (tk.count - base <= 16)
+          columns(std::integral_constant<int, 1>{}, x, y);
+        else
+          columns(std::integral_constant<int, 2>{}, x, y);
+      };
+      if (!flip)
+        tile(r0, r1);
       else
-        Up::template tile<2>(a, st, r0, r1, tk, e, it, base, now, from, to, more || again, then,
-                             sums, turn);
+        tile(r1, r0);
+      flip ^= (to - from) % 2 != 0;
       ++turn;
     }
     now = nt;
@@ -404,7 +449,8 @@ __global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_
     int e = ex.at(rank);
     typename Stream::Tiles now = Down::tiles_of(a, e, n0);
     typename Stream::Rows r0, r1;
-    if (at < st.whole()) st.load_rows(r0, now, at);
+    st.load_rows(r0, now, at);
+    bool flip = false;
     for (int64_t c = from; c < to;) {
       const int n = (int)min((int64_t)(chunks - at), to - c);
       const bool more = c + n < to;
@@ -416,12 +462,20 @@ __global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_
         const bool again = base + 16 * kFewColumns < tk.count;
         const typename Stream::Tiles then = again ? now : nt;
         const int tc = again ? at : 0;
-        if (tk.count - base <= 16)
-          Down::template part<1>(a, st, r0, r1, tk, e, n0, base, now, at, at + n, more || again,
-                                 then, tc, mine);
+        auto part = [&](typename Stream::Rows &x, typename Stream::Rows &y)
+                        __attribute__((always_inline)) {
+          if (tk.count - base <= 16)
+            Down::template part<1>(a, st, x, y, tk, e, n0, base, now, at, at + n, more || again,
+                                   then, tc, mine);
+          else
+            Down::template part<2>(a, st, x, y, tk, e, n0, base, now, at, at + n, more || again,
+                                   then, tc, mine);
+        };
+        if (!flip)
+          part(r0, r1);
         else
-          Down::template part<2>(a, st, r0, r1, tk, e, n0, base, now, at, at + n, more || again,
-                                 then, tc, mine);
+          part(r1, r0);
+        flip ^= n % 2 != 0;
       }
       c += n;
       ++rank;
@@ -449,12 +503,30 @@ hipError_t launch_down(const FewArgs &a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Whether a wavefront takes whole tiles instead of a part of the reduction of
+// each: where there are tiles for all of them, and rows of few chunks, of which
+// a part is soon over, or of 8-bit weights.  Parts and whole, in us: 37 experts
+// of 1001 x 1419, 8-bit weights, 69 and 62; 256 of 7168 x 2048, 8-bit weights,
+// 16 tokens 700 and 640; 64 of 256 x 2048, bf16, 47 and 37, of 1024 x 2048 94
+// and 93, but of 2048 x 2048 169 and 197.
+template <GroupElem EL>
+bool few_whole_tiles(const FewArgs &a, int64_t tiles) {
+  return tiles >= 2 * kNumCus * kUpWaves && (EL == kElemI8 || a.H * 2 <= 2048);
+}
+
 template <GroupElem EL, bool XF16>
 hipError_t launch_few(FewArgs a, hipStream_t st) {
   const int64_t pairs = (int64_t)a.T * a.K;
   const int64_t tiles = std::min<int64_t>(pairs, a.E) * ((a.I + kFewRows - 1) / kFewRows);
-  const int64_t grid = std::min<int64_t>(tiles, 2 * kNumCus);
-  hipLaunchKernelGGL((few_up_kernel<EL, XF16>), dim3((uint32_t)grid), dim3(kUpThreads), 0, st, a);
+  if (few_whole_tiles<EL>(a, tiles)) {
+    const int64_t grid = std::min<int64_t>((tiles + kUpWaves - 1) / kUpWaves, 2 * kNumCus);
+    hipLaunchKernelGGL((few_up_kernel<EL, XF16, 1>), dim3((uint32_t)grid), dim3(kUpThreads), 0, st,
+                       a);
+  } else {
+    const int64_t grid = std::min<int64_t>(tiles, 2 * kNumCus);
+    hipLaunchKernelGGL((few_up_kernel<EL, XF16, kUpWaves>), dim3((uint32_t)grid),
+                       dim3(kUpThreads), 0, st, a);
+  }
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (a.parts > 0) return launch_few_shared(XF16, EL == kElemI8, a, st);
