@@ -188,7 +188,8 @@ class MoE:
         check(lib.cco_moe_get_routing(m, ctypes.byref(r)), "cco_moe_get_routing")
         self.routing_ptrs = r
         self.T = None
-        self._rows8 = False  # the receive windows hold 8-bit rows
+        self._rows8 = False  # the receive windows hold 8-bit rows ..
+        self._scales8 = 0    # .. with so many scales each
 
     @property
     def handle(self) -> ctypes.c_void_p:
@@ -234,7 +235,7 @@ class MoE:
                                        _ptr(scales, torch.float32, "scales"), ns,
                                        _ptr(w, torch.float32, "w"), T, _stream(stream)),
               "cco_moe_dispatch_fp8")
-        self._rows8 = True
+        self._rows8, self._scales8 = True, ns
 
     def expert(self, w13: torch.Tensor | None, w2: torch.Tensor | None, stream=None) -> None:
         """cco_moe_expert; w13 bf16 [E, 2I, H], w2 bf16 [E, H, I]."""
@@ -343,6 +344,22 @@ class MoE:
         ptr = self.heap.slot_ptr(slot, getattr(self.layout, name))
         return _device_tensor(ptr, (rows, width[name]), "<i2", self.heap.device).view(
             torch.bfloat16)
+
+    def window8(self, slot: int, rows: int) -> tuple[torch.Tensor, torch.Tensor]:
+        """After dispatch_fp8, the first `rows` rows of a slot's receive window
+        over the window's own memory (no copy): (codes int8 [rows, H], scales
+        fp32 [rows, ns]), both with the window's row distance.  With rows of
+        quant_rows, codes and scales[:, 0] are operands of group_product_i8.
+        Borrowed: valid until the heap is destroyed."""
+        if not self._rows8:
+            raise ValueError("the receive windows hold no 8-bit rows")
+        if not 0 <= rows <= self.cap or not 0 <= slot < self.S:
+            raise ValueError("slot or rows out of range")
+        ptr = self.heap.slot_ptr(slot, self.layout.disp_x)
+        t = _device_tensor(ptr, (rows, self.H), "<i2", self.heap.device)
+        at = self.H // 4
+        return (t.view(torch.int8)[:, :self.H],
+                t.view(torch.float32)[:, at:at + self._scales8])
 
     def expert_groups(self, slot: int) -> tuple[torch.Tensor, torch.Tensor]:
         """(first, count) int32 [E / S] of the slot's experts: the routing

@@ -156,7 +156,9 @@ int cco_group_product_dw(const cco_groups *g, int32_t dtype, const void *dy, int
  *   q      device int8 [rows][cols], row distance ldq
  *   s      device fp32, one a row at distance lds
  * Columns and row distances lie in [1, 2^21).  The weights of
- * cco_group_product_i8 are such rows too: [groups * n][k] gives w and ws. */
+ * cco_group_product_i8 are such rows too: [groups * n][k] gives w and ws.
+ * cco_moe_dispatch_fp8 moves such rows and their scales as they are;
+ * cco_moe_expert does not take them (its 8-bit rows are e4m3). */
 int cco_quant_rows(const void *x, int32_t dtype, int64_t ldx, int32_t rows, int32_t cols,
                    int32_t swiglu, int8_t *q, int64_t ldq, float *s, int64_t lds, void *stream);
 

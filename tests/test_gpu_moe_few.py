@@ -76,7 +76,7 @@ def test_odd_sizes(cco, dtype, wdtype, H, I):
 @pytest.mark.parametrize("T,H,I,E,K", [(20, 200, 1003, 3, 2), (40, 130, 2048, 2, 1),
                                        (9, 16, 8, 2, 2), (3, 4100, 700, 1, 1),
                                        (1, 4112, 300, 2, 1), (64, 80, 257, 4, 4),
-                                       (64, 72, 520, 64, 2)])
+                                       (64, 72, 520, 64, 2), (64, 4200, 40, 200, 1)])
 def test_both_forms_of_the_down_product(cco, dtype, wdtype, T, H, I, E, K):
     # several parts of the reduction, ends of rows and of column blocks
     say("case: few down %s %s T=%d H=%d I=%d E=%d K=%d" % (dtype, wdtype, T, H, I, E, K))
