@@ -316,10 +316,10 @@ def _distance(t: torch.Tensor, dev, name: str, rows: int) -> int:
     """An fp32 [rows] vector; returns the distance of its elements."""
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError("%s must be a tensor on %s" % (name, dev))
-    if t.shape != (rows,) or t.dtype != torch.float32:
+    if t.shape != (rows,) or t.dtype is not torch.float32:
         raise ValueError("%s must be float32 [%d], got %s %s" % (name, rows, t.dtype,
                                                                 tuple(t.shape)))
-    if rows <= 1:
+    if rows <= 1 or t.is_contiguous():
         return 1
     if t.stride(0) < 1:
         raise ValueError("the elements of %s overlap" % name)
@@ -334,18 +334,20 @@ def _quant(x, halves, out, scales, stream, name):
     ldx = _rows(x, dev, "x")
     code = _dtype(x, "x")
     rows, cols = x.shape
-    if cols % halves:
-        raise ValueError("x must have the gate's and as many up columns, got %d" % cols)
-    cols //= halves
+    if halves == 2:
+        if cols % 2:
+            raise ValueError("x must have the gate's and as many up columns, got %d" % cols)
+        cols //= 2
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    ldq = _rows(out, dev, "out", cols, rows, torch.int8)
+        out, ldq = torch.empty((rows, cols), dtype=torch.int8, device=dev), cols or 1
+    else:
+        ldq = _rows(out, dev, "out", cols, rows, torch.int8)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-    lds = _distance(scales, dev, "scales", rows)
-    check(lib.cco_quant_rows(x.data_ptr(), code, ldx, rows, cols, int(halves == 2),
-                             out.data_ptr(), ldq, scales.data_ptr(), lds,
-                             _raw_stream(dev.index)), name)
+        scales, lds = torch.empty(rows, dtype=torch.float32, device=dev), 1
+    else:
+        lds = _distance(scales, dev, "scales", rows)
+    check(lib.cco_quant_rows(x.data_ptr(), code, ldx, rows, cols, halves - 1, out.data_ptr(), ldq,
+                             scales.data_ptr(), lds, _raw_stream(dev.index)), name)
     return out, scales
 
 
