@@ -195,7 +195,8 @@ int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, cons
  * Ids may repeat in a token (each counts); a pair whose id lies outside
  * [0, E) takes no part, and a token without any gets zeros.  The weights of
  * experts that no token has are not read, and what a token gets does not
- * depend on the others'.  Sums are fp32, h is held to 2^-17 of it, and only
+ * depend on the others'.  Sums are fp32, h is held to 2^-17 of it (in two
+ * parts: where an infinity enters a result, it is infinite or NaN), and only
  * `out` is rounded. */
 typedef struct {
   int32_t hidden;      /* H, 1 .. 2^20 */
