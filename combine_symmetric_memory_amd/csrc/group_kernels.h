@@ -461,6 +461,29 @@ bool small_tiles(const GroupArgs &a) {
   return 3 * even_tiles((GroupOp)OP, 256, a.groups, a.rows, a.n, a.k) < 2 * kNumCus;
 }
 
+// The 8-bit product besides: tiles of 128 where those of 256 end in a round
+// that few CUs take part in.  Groups of uneven rows have about half a row of
+// tiles more each than even ones; a round of 128 x 128 tiles, two a CU, takes
+// 0.575 of one of 256 x 256.  (256 and 128, in us: 8 groups, 4096 rows, 4096 x
+// 4096 99 and 83; 32 groups, 8192 rows, 2048 x 2048 62 and 52; but 8 groups,
+// 8192 rows, 4096 x 14336 547 and 557, 1 group of 8192 rows, 4096 x 7168 203
+// and 230, 256 groups, 65536 rows, 7168 x 2048 1250 and 1450.)  Not for groups
+// of up to 128 rows, whose wide tiles are as small: 8 groups, 1000 rows,
+// 14336 x 4096 108 and 116.
+inline bool short_last_round(const GroupArgs &a) {
+  const int64_t live = std::min<int64_t>(a.groups, a.rows);
+  if (a.rows <= 128 * live) return false;
+  auto rounds = [&](int tile) {
+    const int64_t ct = (a.n + tile - 1) / tile;
+    const int64_t more = live > 1 ? live * ct / (tile == 256 ? 4 : 2) : 0;
+    const int64_t at_once = tile == 256 ? kNumCus : 2 * kNumCus;
+    return (even_tiles(kGroupProduct, tile, a.groups, a.rows, a.n, a.k) + more + at_once - 1) /
+           at_once;
+  };
+  // (0.93: the smaller tiles read more and have to win clearly)
+  return 575 * rounds(128) < 930 * rounds(256);
+}
+
 template <int OP, GroupElem EL, bool F16, bool OUT32>
 hipError_t launch_general(const GroupArgs &a, hipStream_t st) {
   const int64_t tiles = tile_bound<OP, kGenTile>(a);
@@ -563,8 +586,9 @@ template <int OP, GroupElem EL, bool F16, bool OUT32>
 hipError_t launch_either(bool aligned, const GroupArgs &a, hipStream_t st) {
   if (!aligned) return launch_general<OP, EL, F16, OUT32>(a, st);
   if (a.parts > 1) return launch_split<OP, EL, F16, OUT32>(a, st);
-  return small_tiles<OP>(a) ? launch_tiles<OP, EL, F16, OUT32, 128>(a, st)
-                            : launch_tiles<OP, EL, F16, OUT32, 256>(a, st);
+  return small_tiles<OP>(a) || (EL == kElemI8 && short_last_round(a))
+             ? launch_tiles<OP, EL, F16, OUT32, 128>(a, st)
+             : launch_tiles<OP, EL, F16, OUT32, 256>(a, st);
 }
 
 template <int OP>

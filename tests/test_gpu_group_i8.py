@@ -95,6 +95,18 @@ def test_many_tiles_and_wide_tiles(cco, n, k):
     _check(cco, first, count, sum(count), n, k, torch.bfloat16, 5)
 
 
+def test_small_tiles_for_a_short_last_round(cco):
+    # 32 uneven groups of 256 rows on average: 320 tiles of 256 would be two
+    # rounds of the 256 CUs, the second nearly empty
+    g = torch.Generator().manual_seed(8)
+    count = (256 + torch.randint(-60, 61, (32,), generator=g)).tolist()
+    count[3] = 0
+    count[-1] += 8192 - sum(count)
+    first = [sum(count[:i]) for i in range(32)]
+    for dtype in (torch.bfloat16, torch.float32):
+        _check(cco, first, count, 8192, 2048, 144, dtype, 13)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,n,k", [(16, 256, 14336), (40, 512, 8192), (3, 128, 131056)])
 def test_split_reductions(cco, dtype, rows, n, k):
