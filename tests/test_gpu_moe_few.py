@@ -123,6 +123,16 @@ def test_all_tokens_at_one_expert(cco):
     _check(cco, c)
 
 
+@pytest.mark.parametrize("dtype,wdtype", TYPES)
+@pytest.mark.parametrize("T", [17, 33, 64])
+def test_an_expert_with_more_tokens_than_the_others(cco, dtype, wdtype, T):
+    # several rounds of 16 tokens for one expert, none for some
+    c = _case(T, 192, 600, 8, 1, dtype, wdtype, 14)
+    c["idx"][:] = 3
+    c["idx"][5] = 6
+    _check(cco, c)
+
+
 def test_many_experts_and_pairs(cco):
     c = _case(64, 64, 32, 1024, 32, BF, torch.int8, 5)
     _check(cco, c)
