@@ -33,12 +33,13 @@ __device__ __forceinline__ u32x4 load16(GlobalBytes *p) {
 }
 // 16 bytes at p, of which the first `have` exist; the others are zeros.
 __device__ __forceinline__ u32x4 load16(GlobalBytes *p, int have) {
-  if (have >= 16) return load16(p);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < have) v[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
-  return v;
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int i = min(have, 16) - 1; i >= 0; --i) {
+    hi = (hi << 8) | (lo >> 56);
+    lo = (lo << 8) | (uint8_t)p[i];
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 // The 16 bytes at `at` of a row of `bytes` out of 16 loaded from there or, so
 // as to lie inside the row, from bytes - 16: what is behind the end is zeros.

@@ -84,16 +84,23 @@ struct FewStream {
           r.v[u][i] = load16(t.a[i] + (arow[i] + c * U * kFewStepBytes) + u * kFewStepBytes);
       return;
     }
+    if (abytes < 16) {  // all of the row is in the first piece
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          r.v[u][i] = u == 0 ? load16(t.a[i] + (arow[i] - piece * 16), piece == 0 ? abytes : 0)
+                             : u32x4{0, 0, 0, 0};
+      return;
+    }
     // pieces that would pass the row's end take its last 16 bytes
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int at = (c * U + u) * kFewStepBytes + piece * 16;
-        const uint32_t row = arow[i] - piece * 16;
-        r.v[u][i] = abytes >= 16 ? load16(t.a[i] + (row + (uint32_t)min(at, abytes - 16)))
-                                 : load16(t.a[i] + (row + min(at, abytes)), abytes - at);
-      }
+      for (int i = 0; i < MT; ++i)
+        r.v[u][i] = load16(t.a[i] + (arow[i] - piece * 16 +
+                                     (uint32_t)min((c * U + u) * kFewStepBytes + piece * 16,
+                                                   abytes - 16)));
     // (keeps the compiler from one set of loads for both cases, at addresses
     // of 64 bits each)
     asm volatile("" ::: "memory");
@@ -141,10 +148,12 @@ struct FewStream {
               const int in = piece * 16 * HALVES;
               const int at = s + u * kFewStepBytes * HALVES + in + h * 16;
               const uint32_t row = brow[n] - in;
-              if (bbytes >= 16)
+              if (abytes >= 16)
                 col[u][n][h] = end_cut(load16(b + (row + (uint32_t)min(at, bbytes - 16))), at, bbytes);
-              else
-                col[u][n][h] = load16(b + (row + min(at, bbytes)), bbytes - at);
+              else  // (all of it is in the first piece, 32 bytes with 8-bit weights)
+                col[u][n][h] = u0 + u == 0
+                                   ? load16(b + (row + h * 16), piece == 0 ? bbytes - h * 16 : 0)
+                                   : u32x4{0, 0, 0, 0};
               asm volatile("" : "+v"(col[u][n][h]));
             }
       }

@@ -337,14 +337,15 @@ hipError_t launch_shared(const FewArgs &a, hipStream_t st) {
 // 1024 x 1024, top-2: 1 and 4 tokens 16 and 19 (the launch that joins the
 // parts), 16 and 64 tokens 26 and 22, 37 and 28.  One token of 256 experts of
 // 7168 x 2048 125 and 134: there is nothing to share, and the other form's
-// workgroups, one on every CU with 28 columns, need no join.
+// workgroups, one on every CU with 28 columns, need no join; with 8-bit weights
+// 87 and 82.
 int few_parts(bool i8, int32_t T, int32_t K, int32_t E, int32_t H, int32_t I) {
   const int64_t row = (int64_t)I * (i8 ? 1 : 2);
   // what the kernel assumes: whole wavefronts of columns, rows of 16 bytes
   if (H < kFewRows || row < 16) return 0;
   const int64_t experts = std::min<int64_t>((int64_t)T * K, E);
   const bool little = experts * H * row < (24 << 20) && (int64_t)T * K < 2 * (int64_t)E;
-  if (little || (T == 1 && H > 16 * kNumCus)) return 0;
+  if (little || (T == 1 && !i8 && H > 16 * kNumCus)) return 0;
   const int64_t blocks = (H + kFewBlock - 1) / kFewBlock;
   const int64_t chunk = SharedDown<kElemI8>::Stream::CHUNK * (i8 ? 1 : 2);
   const int64_t chunks = experts * ((row + chunk - 1) / chunk);
