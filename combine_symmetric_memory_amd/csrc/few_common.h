@@ -158,13 +158,14 @@ __device__ __forceinline__ u32x4 from_i8(uint32_t lo, uint32_t hi) {
   }
   return r;
 }
-// Eight fp16 values as the sum of two bf16 ones.
+// Eight fp16 values as the sum of two bf16 ones, exactly: the high one is the
+// value to nearest, which leaves at most 2^-8 of it, in three bits.
 __device__ __forceinline__ void split_f16(u32x4 v, u32x4 &hi, u32x4 &lo) {
   const f16x8 h = __builtin_bit_cast(f16x8, v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float a = (float)h[2 * i], b = (float)h[2 * i + 1];
-    hi[i] = top_halves(a, b);
+    hi[i] = pack_half<false>(a, b);
     const float ah = __builtin_bit_cast(float, hi[i] << 16);
     const float bh = __builtin_bit_cast(float, hi[i] & 0xffff0000u);
     lo[i] = top_halves(a - ah, b - bh);
@@ -201,7 +202,8 @@ __device__ __forceinline__ void few_multiply(f32x4 (&acc)[NT], u32x4 w,
     split_f16(w, hi, lo);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      // (the product of the two low parts is 2^-16 of the whole)
+      // (the product of the two low parts, 2^-8 of each, is at most 2^-16 of
+      // the whole: a step of h, or less)
       mma(n, hi, col[n][0]);
       mma(n, hi, col[n][1]);
       mma(n, lo, col[n][0]);
