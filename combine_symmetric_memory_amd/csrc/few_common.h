@@ -216,9 +216,12 @@ __device__ __forceinline__ void few_multiply(f32x4 (&acc)[NT], u32x4 w,
   }
 }
 
-// h as two bf16 values; an infinite or NaN h is whole in its high part.
+// h as two bf16 values, h = hi + lo to 2^-17 of it.  Where h itself is finite
+// and would round to an infinity, bf16's largest value is the high part; an
+// infinite or NaN h is whole in it.
 __device__ __forceinline__ void few_split(float h, uint16_t &hi, uint16_t &lo) {
   hi = f32_to_bf16_rne(h);
+  if (__builtin_fabsf(h) < __builtin_inff() && (hi & 0x7fff) == 0x7f80) --hi;
   const float left = h - from_half_bits<false>(hi);
   lo = __builtin_fabsf(left) < __builtin_inff() ? f32_to_bf16_rne(left) : 0;
 }
