@@ -194,11 +194,13 @@ int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, cons
  *   out[t] = sum_j w[t][j] * W2_e h
  * Ids may repeat in a token (each counts); a pair whose id lies outside
  * [0, E) takes no part, and a token without any gets zeros.  The weights of
- * experts that no token has are not read, and what a token gets does not
- * depend on the others'.  Sums are fp32, h is held to 2^-17 of it (in two
- * parts: where an infinity enters a result, it is infinite or NaN), fp16
- * weights leave out at most 2^-16 of each term of the second product, and
- * only `out` is rounded. */
+ * experts that no token has are not read, and no value of another token
+ * enters what a token gets: infinities and NaN stay with their tokens.  (The
+ * order of its sums, and so its last bits, depend on T and on the experts in
+ * use; the same call gives the same bits.)
+ *   Sums are fp32, h is held to 2^-17 of it (in two parts: where an infinity
+ * enters a result, it is infinite or NaN), fp16 weights leave out at most
+ * 2^-16 of each term of the second product, and only `out` is rounded. */
 typedef struct {
   int32_t hidden;      /* H, 1 .. 2^20 */
   int32_t inter;       /* I, 1 .. 2^19 */
