@@ -137,6 +137,7 @@ struct FewTokens {
   }
 };
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // Two bf16 halves of the top 16 bits of a and b.
 __device__ __forceinline__ uint32_t top_halves(float a, float b) {
   return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a),
@@ -165,7 +166,7 @@ __device__ __forceinline__ void split_f16(u32x4 v, u32x4 &hi, u32x4 &lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float a = (float)h[2 * i], b = (float)h[2 * i + 1];
-    hi[i] = pack_half<false>(a, b);
+    hi[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
     const float ah = __builtin_bit_cast(float, hi[i] << 16);
     const float bh = __builtin_bit_cast(float, hi[i] & 0xffff0000u);
     lo[i] = top_halves(a - ah, b - bh);
