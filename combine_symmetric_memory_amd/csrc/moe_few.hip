@@ -45,11 +45,19 @@ constexpr int kFewColumns = 2;
 // it the same expert's or the next one's, are in flight while a chunk is
 // multiplied; its columns, which the caches hold, are issued before them and
 // waited for alone, UB steps at a time, so that they take few registers.
-template <GroupElem EL, bool PAIR, bool XF16, int MT>
+//
+// Weight rows of fewer than 16 bytes are read byte by byte: in the down product
+// (PAIR) by kernels of their own (TINY), since beside the other loads that path
+// cost its kernels 12 to 68 bytes of scratch a lane (4 tokens, 8 experts of
+// 256 x 512, fp16: 8.9 us, without 6.6; one token of 256 of 7168 x 2048 in all
+// 135 and 130), in the gate and up product beside them, which took the same
+// change badly (64 tokens, 8 experts of 4096 x 14336, in all 613 and 625).
+template <GroupElem EL, bool PAIR, bool XF16, int MT, bool TINY>
 struct FewStream {
+  static_assert(PAIR || !TINY, "");
   static constexpr int HALVES = EL == kElemI8 ? 2 : 1;  // 16-byte pieces of a column a step
   static constexpr int NB = (PAIR ? 2 : 1) * HALVES;
-  static constexpr int U = PAIR && EL == kElemI8 ? 4 : 8 / MT;
+  static constexpr int U = TINY ? 1 : PAIR && EL == kElemI8 ? 4 : 8 / MT;
   // pieces of columns in registers at once; conversions need some themselves
   static constexpr int kColumnPieces = EL == kElemI8 ? 8 : 16;
   template <int NT>
@@ -76,6 +84,12 @@ struct FewStream {
   }
 
   __device__ __forceinline__ void load_rows(Rows &r, const Tiles &t, int c) const {
+    if constexpr (TINY) {  // all of the row is in the first piece
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        r.v[0][i] = load16(t.a[i] + (arow[i] - piece * 16), piece == 0 ? abytes : 0);
+      return;
+    }
     if (!ends(c)) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -84,7 +98,7 @@ struct FewStream {
           r.v[u][i] = load16(t.a[i] + (arow[i] + c * U * kFewStepBytes) + u * kFewStepBytes);
       return;
     }
-    if (abytes < 16) {  // all of the row is in the first piece
+    if (!PAIR && abytes < 16) {  // all of the row is in the first piece
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -107,7 +121,7 @@ struct FewStream {
   }
   // What lies behind the row's end in its last chunk becomes zeros.
   __device__ __forceinline__ void cut_rows(Rows &r, int c) const {
-    if (abytes < 16) return;
+    if (TINY || (!PAIR && abytes < 16)) return;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -203,7 +217,7 @@ struct UpSums {
 
 template <GroupElem EL, bool XF16, int PARTS>
 struct FewUp {
-  using Stream = FewStream<EL, false, XF16, 2>;
+  using Stream = FewStream<EL, false, XF16, 2, false>;
   static constexpr int ES = EL == kElemI8 ? 1 : 2;
 
   __device__ static __forceinline__ typename Stream::Tiles tiles_of(const FewArgs &a, int e,
@@ -368,9 +382,9 @@ __global__ __launch_bounds__(kUpThreads, 2) void few_up_kernel(FewArgs a) {
 // wavefronts split the reduction over all experts in use, end to end, into
 // equal ranges; each keeps its own sums of the tokens in LDS, and they are
 // added up in order.
-template <GroupElem EL, int MT>
+template <GroupElem EL, int MT, bool TINY>
 struct FewDown {
-  using Stream = FewStream<EL, true, false, MT>;
+  using Stream = FewStream<EL, true, false, MT, TINY>;
   static constexpr int ES = EL == kElemI8 ? 1 : 2;
   static constexpr int SUMS = MT * kFewRows;  // sums of a token
 
@@ -424,20 +438,21 @@ struct FewDown {
   }
 };
 
-template <GroupElem EL, bool XF16, int MT, int WAVES>
-__global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_down_kernel(
-    FewArgs a) {
-  using Down = FewDown<EL, MT>;
+constexpr int kDownWaves = 8, kDownThreads = kDownWaves * kWave;
+
+template <GroupElem EL, bool XF16, int MT, bool TINY>
+__device__ __forceinline__ void few_down(const FewArgs &a) {
+  using Down = FewDown<EL, MT, TINY>;
   using Stream = typename Down::Stream;
   constexpr int SUMS = Down::SUMS;
   __shared__ uint32_t id_words[FewIds::words(kFewMaxTokens * kMaxTopk)];
   const FewIds s(id_words, a.T * a.K);
-  extern __shared__ __align__(16) float sums[];  // [WAVES][T][SUMS]
+  extern __shared__ __align__(16) float sums[];  // [kDownWaves][T][SUMS]
   const int wave = uniform((int)threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int n0 = blockIdx.x * a.cols;
   float *mine = sums + wave * a.T * SUMS;
   for (int i = lane; i < a.T * SUMS; i += kWave) mine[i] = 0.0f;
-  few_read_ids<WAVES * kWave>(a, s);
+  few_read_ids<kDownThreads>(a, s);
   const FewExperts ex(s);
   Stream st;
   st.abytes = a.I * Down::ES;
@@ -452,7 +467,7 @@ __global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_
                  st.piece * 16;
   const int chunks = st.chunks();
   const int64_t all = (int64_t)ex.count * chunks;
-  const int64_t from = all * wave / WAVES, to = all * (wave + 1) / WAVES;
+  const int64_t from = all * wave / kDownWaves, to = all * (wave + 1) / kDownWaves;
   if (from < to) {
     int rank = (int)(from / chunks), at = (int)(from - (int64_t)rank * chunks);
     int e = ex.at(rank);
@@ -494,21 +509,29 @@ __global__ __launch_bounds__(WAVES *kWave, WAVES <= 8 ? 2 : WAVES / 4) void few_
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.T * SUMS; i += WAVES * kWave) {
+  for (int i = threadIdx.x; i < a.T * SUMS; i += kDownThreads) {
     const int t = i / SUMS, n = i % SUMS;
     float v = sums[i];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) v += sums[w * a.T * SUMS + i];
+    for (int w = 1; w < kDownWaves; ++w) v += sums[w * a.T * SUMS + i];
     if (n < a.cols && n0 + n < a.H)
       ((uint16_t *)a.out)[(int64_t)t * a.H + n0 + n] = to_half_bits<XF16>(v);
   }
 }
 
-template <GroupElem EL, bool XF16, int MT, int WAVES>
-hipError_t launch_down(const FewArgs &a, hipStream_t st) {
-  const int lds = WAVES * a.T * MT * kFewRows * (int)sizeof(float);
-  hipLaunchKernelGGL((few_down_kernel<EL, XF16, MT, WAVES>),
-                     dim3((uint32_t)((a.H + a.cols - 1) / a.cols)), dim3(WAVES * kWave), lds, st, a);
+template <GroupElem EL, bool XF16, int MT>
+__global__ __launch_bounds__(kDownThreads, 2) void few_down_kernel(FewArgs a) {
+  few_down<EL, XF16, MT, false>(a);
+}
+template <GroupElem EL, bool XF16>
+__global__ __launch_bounds__(kDownThreads, 2) void few_tiny_down_kernel(FewArgs a) {
+  few_down<EL, XF16, 1, true>(a);
+}
+
+hipError_t launch_down(void (*kernel)(FewArgs), const FewArgs &a, int sums, hipStream_t st) {
+  const int lds = kDownWaves * a.T * sums * (int)sizeof(float);
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)((a.H + a.cols - 1) / a.cols)), dim3(kDownThreads),
+                     lds, st, a);
   return hipGetLastError();
 }
 
@@ -539,11 +562,15 @@ hipError_t launch_few(FewArgs a, hipStream_t st) {
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   if (a.parts > 0) return launch_few_shared(XF16, EL == kElemI8, a, st);
+  if (a.I * (EL == kElemI8 ? 1 : 2) < 16) {
+    a.cols = kFewRows;
+    return launch_down(few_tiny_down_kernel<EL, XF16>, a, kFewRows, st);
+  }
   // one workgroup on every CU, or whole rounds of them
   const int rounds = (a.H + 32 * kNumCus - 1) / (32 * kNumCus);
   a.cols = std::max(kFewRows, (a.H + rounds * kNumCus - 1) / (rounds * kNumCus));
-  return a.cols > kFewRows ? launch_down<EL, XF16, 2, 8>(a, st)
-                           : launch_down<EL, XF16, 1, 8>(a, st);
+  return a.cols > kFewRows ? launch_down(few_down_kernel<EL, XF16, 2>, a, 2 * kFewRows, st)
+                           : launch_down(few_down_kernel<EL, XF16, 1>, a, kFewRows, st);
 }
 
 }  // namespace
