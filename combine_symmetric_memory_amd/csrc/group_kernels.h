@@ -462,14 +462,15 @@ bool small_tiles(const GroupArgs &a) {
 }
 
 // The 8-bit product besides: tiles of 128 where those of 256 end in a round
-// that few CUs take part in.  Groups of uneven rows have about half a row of
-// tiles more each than even ones; a round of 128 x 128 tiles, two a CU, takes
-// 0.575 of one of 256 x 256.  (256 and 128, in us: 8 groups, 4096 rows, 4096 x
-// 4096 99 and 83; 32 groups, 8192 rows, 2048 x 2048 62 and 52; but 8 groups,
-// 8192 rows, 4096 x 14336 547 and 557, 1 group of 8192 rows, 4096 x 7168 203
-// and 230, 256 groups, 65536 rows, 7168 x 2048 1250 and 1450.)  Not for groups
-// of up to 128 rows, whose wide tiles are as small: 8 groups, 1000 rows,
-// 14336 x 4096 108 and 116.
+// that few CUs take part in.  A group of uneven rows ends anywhere in a row of
+// tiles and has on average half of one more than its rows fill; with tiles of
+// 256 a quarter, since up to 128 rows take half as many tiles, wide ones.  A
+// round of 128 x 128 tiles, two a CU, takes 0.575 of one of 256 x 256.  (256
+// and 128, in us: 8 groups, 4096 rows, 4096 x 4096 100 and 85; 32 groups, 8192
+// rows, 2048 x 2048 60 and 53; but 8 groups, 8192 rows, 4096 x 14336 538 and
+// 553, 1 group of 8192 rows, 4096 x 7168 195 and 230, 256 groups, 65536 rows,
+// 7168 x 2048 1221 and 1468.)  Not for groups of up to 128 rows, whose wide
+// tiles are as small: 8 groups, 1000 rows, 14336 x 4096 104 and 110.
 inline bool short_last_round(const GroupArgs &a) {
   const int64_t live = std::min<int64_t>(a.groups, a.rows);
   if (a.rows <= 128 * live) return false;

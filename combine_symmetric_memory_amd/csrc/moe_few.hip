@@ -4,7 +4,8 @@
 //   h[t, e] = silu(Wg_e x[t]) * (Wu_e x[t])
 //   out[t]  = sum_e share[t][e] W2_e h[t, e]
 //
-// Bound by the weights of the experts that some token has, each read once.
+// Bound by the weights of the experts that some token has, each read once, and
+// again, mostly from the caches, for every further 32 tokens of an expert.
 // Nothing is planned beforehand: every workgroup finds the experts in use and
 // their tokens from the ids (a bit set of experts; the tokens of an expert are
 // one ballot, so there are at most 64).
@@ -21,12 +22,22 @@
 // eleven bits into two bf16 values), so that h may exceed fp16's range.
 // 8-bit weights are exact in bf16 and fp16 and meet their scales in the sums.
 //
-// What carries the stream is that a wavefront always has the next 8 KiB of
-// weights in flight, over the ends of tiles and experts too, with eight
-// wavefronts a CU that need 256 registers a lane for it: 16 wavefronts of 128
-// registers, which spill, took 1.25 to 1.4 times as long, chunks of 16 KiB 1.1
-// to 1.4 times.  One token of 256 experts of 7168 x 2048, top-8, bf16: gate
-// and up 5.9 TB/s, down 5.2; 16 tokens with 8-bit weights 6.8 TB/s in all.
+// What carries the stream is that a wavefront asks for the next 8 KiB of
+// weights before it multiplies a chunk, over the ends of tiles and experts too,
+// with eight wavefronts a CU that need 256 registers a lane for it: 16
+// wavefronts of 128 registers, which spill, took 1.25 to 1.4 times as long,
+// chunks of 16 KiB 1.1 to 1.4 times.  The weights do not stay in flight
+// throughout: by a chunk's last product the compiler's waits for its columns
+// are for everything (it counts the paths of a row's middle and of its end as
+// one), a tile or an expert begins with rows moved between registers behind
+// such a wait, the scales of 8-bit gate and up weights are read behind the next
+// tile's rows, and the kernels that spill (8-bit weights: gate and up split over
+// wavefronts, 84 bytes a lane, down with two tiles of rows, 44; fp16: the
+// latter, 20) reload between tiles and experts.  The CU's other wavefronts
+// cover that.
+// Of the experts in use, one token of 256 of 7168 x 2048, top-8, bf16: gate and
+// up 5.9 TB/s, down 5.4; 16 tokens with 8-bit weights 5.5 and, in the form with
+// shared rows, 4.6.
 #include "few_common.h"
 
 namespace cco {
@@ -42,9 +53,9 @@ constexpr int kFewColumns = 2;
 // bf16.
 //
 // The reduction goes by chunks of U steps.  The weights of the next chunk, be
-// it the same expert's or the next one's, are in flight while a chunk is
-// multiplied; its columns, which the caches hold, are issued before them and
-// waited for alone, UB steps at a time, so that they take few registers.
+// it the same expert's or the next one's, are asked for before a chunk is
+// multiplied, behind its columns, which the caches hold and which come UB steps
+// at a time, so that they take few registers.
 //
 // Weight rows of fewer than 16 bytes are read byte by byte: in the down product
 // (PAIR) by kernels of their own (TINY), since beside the other loads that path

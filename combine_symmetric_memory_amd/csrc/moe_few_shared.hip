@@ -4,8 +4,10 @@
 //
 // The four wavefronts of a workgroup take 16 output columns each over the same
 // stretch of the reduction and share its tokens' rows of h in LDS, which
-// direct loads fill a chunk ahead; a chunk's weights are in registers a chunk
-// ahead too.  Each wavefront for itself, as in the other form, loads one to
+// direct loads fill a chunk ahead; a chunk's weights are asked for a chunk
+// ahead too, and the barrier between chunks waits for both.  (At a segment's
+// end rows move between registers behind such a wait, and 8-bit weights' scales
+// are read behind the next segment's rows.)  Each wavefront for itself, as in the other form, loads one to
 // four times the weights' bytes of h over its compute unit's load path,
 // whatever the number of tokens (the columns that none fills included).  A
 // workgroup takes one part of the reduction over all experts in use; the
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_shared_down_kernel(FewArgs a,
   }
 }
 
-// out = the parts' sums, in order; four columns a thread where H allows.
+// out = the parts' sums, in order; one element a thread.
 template <bool XF16>
 __global__ __launch_bounds__(256) void few_join_kernel(FewArgs a) {
   const int64_t all = (int64_t)a.T * a.H;
@@ -335,10 +337,14 @@ hipError_t launch_shared(const FewArgs &a, hipStream_t st) {
 // 2048 x 1024, top-8, 1 token 27 and 26, 2 tokens 46 and 40, 8 tokens 132 and
 // 106; 8 experts of 4096 x 14336, top-2, 8 tokens 543 and 520; 8 of
 // 1024 x 1024, top-2: 1 and 4 tokens 16 and 19 (the launch that joins the
-// parts), 16 and 64 tokens 26 and 22, 37 and 28.  One token of 256 experts of
-// 7168 x 2048 125 and 134: there is nothing to share, and the other form's
-// workgroups, one on every CU with 28 columns, need no join; with 8-bit weights
-// 87 and 82.
+// parts), 16 and 64 tokens 26 and 22, 37 and 28.  One token with 16-bit weights:
+// the other form's workgroups need no join and, where 16 columns each do not
+// cover H, are one on every CU; 256 experts of H x 2048, top-8, bf16: H 2048 47
+// and 39, 4096 80 and 77, 5120 94 and 97, 7168 129 and 133 (fp16 134 and 144).
+// The rule goes by H alone: longer rows and more than one round of that form's
+// workgroups are for this one (8 of 5120 x 14336 160 and 156, 128 of
+// 10240 x 2048 185 and 179).  With 8-bit weights H 2048 40 and 35, 4160 57 and
+// 53, 7168 89 and 91, 10240 132 and 120.
 int few_parts(bool i8, int32_t T, int32_t K, int32_t E, int32_t H, int32_t I) {
   const int64_t row = (int64_t)I * (i8 ? 1 : 2);
   // what the kernel assumes: whole wavefronts of columns, rows of 16 bytes
@@ -349,7 +355,10 @@ int few_parts(bool i8, int32_t T, int32_t K, int32_t E, int32_t H, int32_t I) {
   const int64_t blocks = (H + kFewBlock - 1) / kFewBlock;
   const int64_t chunk = SharedDown<kElemI8>::Stream::CHUNK * (i8 ? 1 : 2);
   const int64_t chunks = experts * ((row + chunk - 1) / chunk);
-  // two workgroups a CU, parts of four chunks at least
+  // two workgroups a CU, parts of four chunks at least.  (With 32 columns a
+  // segment the LDS of 60 tokens of two experts each, or 51 of eight, leaves
+  // room for one a CU, and the grid runs as two rounds: 3.3 TB/s of weights at
+  // 64 tokens of 8 experts of 4096 x 14336, 4.6 at 16 tokens of 256.)
   const int64_t want = (2 * kNumCus + blocks / 2) / blocks;
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, chunks / 4), 32));
 }

@@ -150,7 +150,8 @@ int cco_group_product_dw(const cco_groups *g, int32_t dtype, const void *dy, int
  * zeros and s = 0; a row that holds a NaN or an infinity gets zeros and
  * s = NaN, so that every product of it is NaN.
  *   v      x[r][c], or with `swiglu` silu(x[r][c]) * x[r][cols + c] of rows
- *          of 2 cols (gate, then up), in fp32
+ *          of 2 cols (gate, then up), in fp32 (a gate below -87, whose
+ *          sigmoid is under fp32's normal range, counts as -0)
  *   x      [rows] of `dtype` (bf16, fp16 or fp32), row distance ldx,
  *          aligned to an element
  *   q      device int8 [rows][cols], row distance ldq
@@ -190,7 +191,7 @@ int cco_group_product_i8(const cco_groups *g, const int8_t *x, int64_t ldx, cons
 
 /* A whole layer in two or three launches, for batches of at most 64 tokens:
  * what plan, dispatch, expert and combine give, without a heap:
- *   h      = silu(Wg_e x[t]) * (Wu_e x[t]),  e = idx[t][j]
+ *   h      = silu(Wg_e x[t]) * (Wu_e x[t]),  e = idx[t][j]  (silu as above)
  *   out[t] = sum_j w[t][j] * W2_e h
  * Ids may repeat in a token (each counts); a pair whose id lies outside
  * [0, E) takes no part, and a token without any gets zeros.  The weights of
