@@ -204,7 +204,7 @@ __device__ __forceinline__ void few_multiply(f32x4 (&acc)[NT], u32x4 w,
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       // (the product of the two low parts, 2^-8 of each, is at most 2^-16 of
-      // the whole: a step of h, or less)
+      // the whole)
       mma(n, hi, col[n][0]);
       mma(n, hi, col[n][1]);
       mma(n, lo, col[n][0]);

@@ -7,10 +7,10 @@
 // direct loads fill a chunk ahead; a chunk's weights are asked for a chunk
 // ahead too, and the barrier between chunks waits for both.  (At a segment's
 // end rows move between registers behind such a wait, and 8-bit weights' scales
-// are read behind the next segment's rows.)  Each wavefront for itself, as in the other form, loads one to
-// four times the weights' bytes of h over its compute unit's load path,
-// whatever the number of tokens (the columns that none fills included).  A
-// workgroup takes one part of the reduction over all experts in use; the
+// are read behind the next segment's rows.)  Each wavefront for itself, as in
+// the other form, loads one to four times the weights' bytes of h over its
+// compute unit's load path, whatever the number of tokens (the columns that
+// none fills included).  A workgroup takes one part of the reduction over all experts in use; the
 // parts' sums, a few MB, are added up by another launch.
 //
 // Measured (down product alone): 8 experts of 4096 x 14336, 16 tokens each:

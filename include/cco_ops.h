@@ -150,8 +150,9 @@ int cco_group_product_dw(const cco_groups *g, int32_t dtype, const void *dy, int
  * zeros and s = 0; a row that holds a NaN or an infinity gets zeros and
  * s = NaN, so that every product of it is NaN.
  *   v      x[r][c], or with `swiglu` silu(x[r][c]) * x[r][cols + c] of rows
- *          of 2 cols (gate, then up), in fp32 (a gate below -87, whose
- *          sigmoid is under fp32's normal range, counts as -0)
+ *          of 2 cols (gate, then up), in fp32 (the product with a finite
+ *          gate below -87.3, whose sigmoid is under fp32's normal range, is
+ *          zero)
  *   x      [rows] of `dtype` (bf16, fp16 or fp32), row distance ldx,
  *          aligned to an element
  *   q      device int8 [rows][cols], row distance ldq
